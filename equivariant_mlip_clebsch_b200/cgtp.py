@@ -59,6 +59,17 @@ _SIGS = {
     "cgtp_sparse_workspace_size": (_i, [_P, _i64, _i64, _i64, ctypes.POINTER(_sz)]),
     "cgtp_sparse_forward": (_i, [_P, _i64, _i64, _i64] + [_P] * 8 + [_sz, _P]),
     "cgtp_sparse_backward": (_i, [_P, _i64, _i64, _i64] + [_P] * 14 + [_sz, _P]),
+    "cgtp_norm_create": (_i, [ctypes.c_char_p, _d, ctypes.POINTER(_P)]),
+    "cgtp_norm_destroy": (_i, [_P]),
+    "cgtp_norm_info": (_i, [_P, _pi64, _pi64, _pi64]),
+    "cgtp_norm_forward": (_i, [_P, _i64] + [_P] * 5),
+    "cgtp_norm_workspace_size": (_i, [_P, _i64, ctypes.POINTER(_sz)]),
+    "cgtp_norm_backward": (_i, [_P, _i64] + [_P] * 7 + [_sz, _P]),
+    "cgtp_norm_double_backward": (_i, [_P, _i64] + [_P] * 10 + [_sz, _P]),
+    "cgtp_router_create": (_i, [_i] * 7 + [_d, ctypes.POINTER(_P)]),
+    "cgtp_router_destroy": (_i, [_P]),
+    "cgtp_router_forward": (_i, [_P, _i64] + [_P] * 5 + [_i64, _P, _P]),
+    "cgtp_router_backward": (_i, [_P, _i64] + [_P] * 4 + [_i64, _P, _P]),
     "cgtp_fma_peak_sink_floats": (_i, [_pi64]),
     "cgtp_fma_peak": (_i, [_i64, _P, _i64, _P, ctypes.POINTER(_d)]),
     "cgtp_neighbor_list": (_i, [_i64, _P, _P, _d, _P, _P, _P, _P, _pi64]),
@@ -126,6 +137,17 @@ def _stream(stream=None):
     import torch
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _on_current(dev, stream):
+    """The calls of handles that belong to no device launch on the current
+    one: refuse arrays or a stream of another."""
+    import torch
+    if dev.type == "cuda":
+        if dev.index != torch.cuda.current_device():
+            raise ValueError(f"the arrays are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"the arrays are on {dev}, the stream is on {stream.device}")
 
 
 def real_cg(l1: int, l2: int, l3: int) -> np.ndarray:
@@ -462,3 +484,177 @@ class Plan:
                                                                       n_send, E),
                                                  _stream(stream)))
         return dx, dW, dY
+
+
+class LayerNorm:
+    """cgtp_norm_*: layer norm of irreps rows x [n, D].  Every block of every
+    row is normalised by itself: 0e blocks are centred and have a weight and a
+    bias per channel, the others are divided by their root mean square and
+    have a weight per channel ("64x0e" is the plain layer norm of 64 columns).
+    weight [n_weight] and bias [n_bias] may be None (ones, zeros)."""
+
+    def __init__(self, irreps: str, eps: float = 1e-5):
+        h = ctypes.c_void_p()
+        _check(_lib.cgtp_norm_create(irreps.encode(), float(eps), ctypes.byref(h)))
+        self._h = h
+        self.irreps, self.eps = irreps, float(eps)
+        v = [ctypes.c_int64() for _ in range(3)]
+        _check(_lib.cgtp_norm_info(h, *[ctypes.byref(t) for t in v]))
+        self.d, self.n_weight, self.n_bias = (t.value for t in v)
+
+    def close(self):
+        if getattr(self, "_h", None):
+            _lib.cgtp_norm_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def forward(self, x, weight=None, bias=None, out=None, stream=None):
+        import torch
+        n, dev = x.shape[0], x.device
+        if out is None:
+            out = torch.empty((n, self.d), dtype=torch.float32, device=dev)
+        ptrs = _args(dev, (x, "x", n * self.d, "f32"), (weight, "weight", self.n_weight, "f32"),
+                     (bias, "bias", self.n_bias, "f32"), (out, "out", n * self.d, "f32"))
+        _on_current(dev, stream)
+        _check(_lib.cgtp_norm_forward(self._h, n, *ptrs, _stream(stream)))
+        return out
+
+    def workspace_size(self, n: int) -> int:
+        b = ctypes.c_size_t()
+        _check(_lib.cgtp_norm_workspace_size(self._h, n, ctypes.byref(b)))
+        return b.value
+
+    def _ws(self, workspace, n, dev):
+        if workspace is None:
+            import torch
+            workspace = torch.empty(max(self.workspace_size(n), 256), dtype=torch.uint8, device=dev)
+        return _workspace(workspace, dev)
+
+    def backward(self, x, weight, grad_out, want=("x", "weight", "bias"), grads=None, workspace=None,
+                 stream=None):
+        """(grad_x, grad_weight, grad_bias) for grad_out = dL/dy."""
+        import torch
+        n, dev = x.shape[0], x.device
+        if grads is None:
+            f = lambda *shape: torch.empty(shape, dtype=torch.float32, device=dev)
+            grads = (f(n, self.d) if "x" in want else None, f(self.n_weight) if "weight" in want else None,
+                     f(self.n_bias) if "bias" in want else None)
+        dx, dw, db = grads
+        ptrs = _args(dev, (x, "x", n * self.d, "f32"), (weight, "weight", self.n_weight, "f32"),
+                     (grad_out, "grad_out", n * self.d, "f32"), (dx, "grad_x", n * self.d, "f32"),
+                     (dw, "grad_weight", self.n_weight, "f32"), (db, "grad_bias", self.n_bias, "f32"))
+        _on_current(dev, stream)
+        _check(_lib.cgtp_norm_backward(self._h, n, *ptrs, *self._ws(workspace, n, dev), _stream(stream)))
+        return dx, dw, db
+
+    def double_backward(self, x, weight, grad_out, h_x=None, h_weight=None, h_bias=None,
+                        want=("g", "x", "weight"), grads=None, workspace=None, stream=None):
+        """The gradients (d grad_out, dx, dweight) of S = <h_x, grad_x> +
+        <h_weight, grad_weight> + <h_bias, grad_bias> over the backward; None
+        cotangents are zero."""
+        import torch
+        n, dev = x.shape[0], x.device
+        if grads is None:
+            f = lambda *shape: torch.empty(shape, dtype=torch.float32, device=dev)
+            grads = (f(n, self.d) if "g" in want else None, f(n, self.d) if "x" in want else None,
+                     f(self.n_weight) if "weight" in want else None)
+        gg, gx, gw = grads
+        ptrs = _args(dev, (x, "x", n * self.d, "f32"), (weight, "weight", self.n_weight, "f32"),
+                     (grad_out, "grad_out", n * self.d, "f32"), (h_x, "h_x", n * self.d, "f32"),
+                     (h_weight, "h_weight", self.n_weight, "f32"), (h_bias, "h_bias", self.n_bias, "f32"),
+                     (gg, "grad_grad_out", n * self.d, "f32"), (gx, "grad_x", n * self.d, "f32"),
+                     (gw, "grad_weight", self.n_weight, "f32"))
+        _on_current(dev, stream)
+        _check(_lib.cgtp_norm_double_backward(self._h, n, *ptrs, *self._ws(workspace, n, dev), _stream(stream)))
+        return gg, gx, gw
+
+
+class Router:
+    """cgtp_router_*: routing of rows (edges) to their k best of n_experts.
+    gates[e] is the gate array of Plan.sparse_forward for expert e, and the
+    rows of grad_gates are what Plan.sparse_backward gives as grad_gate."""
+
+    SCORES = {"softmax": 0, "sigmoid": 1}
+
+    def __init__(self, n_experts: int, k: int, score: str = "softmax", n_groups: int = 1, top_groups: int = 1,
+                 group_best: int = 2, renormalise: bool = True, scale: float = 1.0):
+        if score not in self.SCORES:
+            raise ValueError(f"score: expected one of {sorted(self.SCORES)}, got {score!r}")
+        h = ctypes.c_void_p()
+        _check(_lib.cgtp_router_create(int(n_experts), int(k), self.SCORES[score], int(n_groups), int(top_groups),
+                                       int(group_best), int(bool(renormalise)), float(scale), ctypes.byref(h)))
+        self._h = h
+        self.n_experts, self.k = int(n_experts), int(k)
+
+    def close(self):
+        if getattr(self, "_h", None):
+            _lib.cgtp_router_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _gates(self, t, name, n, dev):
+        """Pointer and row stride of a [n_experts, n] tensor of unit column
+        stride (rows may be padded)."""
+        import torch
+        if t is None:
+            return None, max(n, 4)
+        if t.dtype != torch.float32:
+            raise TypeError(f"{name}: expected torch.float32, got {t.dtype}")
+        if tuple(t.shape) != (self.n_experts, n):
+            raise ValueError(f"{name}: expected shape {(self.n_experts, n)}, got {tuple(t.shape)}")
+        if not t.is_cuda or (n > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name}: expected a CUDA tensor with contiguous rows")
+        if t.device != dev:
+            raise ValueError(f"{name}: on {t.device}, the other arguments on {dev}")
+        ld = t.stride(0) if self.n_experts > 1 and n > 0 else -(-n // 4) * 4
+        if ld < n:
+            raise ValueError(f"{name}: rows overlap (stride {ld}, {n} columns)")
+        return ctypes.c_void_p(t.data_ptr()), ld
+
+    def forward(self, logits, bias=None, want=("ids", "weights", "gates", "counts"), outs=None, stream=None):
+        """(ids [n, k] int32, weights [n, k], gates [n_experts, n], counts
+        [n_experts] int32) of logits [n, n_experts].  The rows of gates are
+        16-byte aligned (their stride is n rounded up to 4)."""
+        import torch
+        n, dev = logits.shape[0], logits.device
+        if outs is None:
+            e = lambda dtype, *shape: torch.empty(shape, dtype=dtype, device=dev)
+            ld = -(-n // 4) * 4
+            outs = (e(torch.int32, n, self.k) if "ids" in want else None,
+                    e(torch.float32, n, self.k) if "weights" in want else None,
+                    e(torch.float32, self.n_experts, ld)[:, :n] if "gates" in want else None,
+                    e(torch.int32, self.n_experts) if "counts" in want else None)
+        ids, weights, gates, counts = outs
+        pl, pb, pi, pw, pc = _args(dev, (logits, "logits", n * self.n_experts, "f32"),
+                                   (bias, "bias", self.n_experts, "f32"), (ids, "ids", n * self.k, "i32"),
+                                   (weights, "weights", n * self.k, "f32"),
+                                   (counts, "counts", self.n_experts, "i32"))
+        pg, ld = self._gates(gates, "gates", n, dev)
+        _on_current(dev, stream)
+        _check(_lib.cgtp_router_forward(self._h, n, pl, pb, pi, pw, pg, ld, pc, _stream(stream)))
+        return ids, weights, gates, counts
+
+    def backward(self, logits, ids, grad_weights=None, grad_gates=None, grad_logits=None, stream=None):
+        """grad_logits [n, n_experts] for grad_weights [n, k] and / or
+        grad_gates [n_experts, n] (rows may be padded)."""
+        import torch
+        n, dev = logits.shape[0], logits.device
+        if grad_logits is None:
+            grad_logits = torch.empty((n, self.n_experts), dtype=torch.float32, device=dev)
+        pl, pi, pw, po = _args(dev, (logits, "logits", n * self.n_experts, "f32"), (ids, "ids", n * self.k, "i32"),
+                               (grad_weights, "grad_weights", n * self.k, "f32"),
+                               (grad_logits, "grad_logits", n * self.n_experts, "f32"))
+        pg, ld = self._gates(grad_gates, "grad_gates", n, dev)
+        _on_current(dev, stream)
+        _check(_lib.cgtp_router_backward(self._h, n, pl, pi, pw, pg, ld, po, _stream(stream)))
+        return grad_logits

@@ -339,6 +339,139 @@ cgtp_status cgtp_sparse_backward(cgtp_plan plan, int64_t n_recv, int64_t n_send,
                                  float* grad_x, float* grad_W, float* grad_Y, float* grad_gate,
                                  void* workspace, size_t workspace_bytes, cgtp_stream stream);
 
+/* ---- layer norm of irreps rows ------------------------------------------ */
+
+/* The normalisation between two convolutions: x [n, D] holds rows of irreps
+ * blocks in order, each [mul, 2l+1] (the layout of the convolution's x and
+ * out), and every block of every row is normalised by itself.  For a block of
+ * N = mul (2l+1) values, c = 1 for 0e blocks (centred) and 0 for all others
+ * (their mean would not be equivariant):
+ *   mu = c mean(x)   xc = x - mu   r = (mean(xc^2) + eps)^(-1/2)   xh = r xc
+ *   y[u, m] = xh[u, m] weight[u] (+ bias[u] on 0e blocks)
+ * "Dx0e" is the plain layer norm of D columns.  The map commutes with
+ * rotations and, with every parity, with inversion.
+ *   weight [n_weight]  one per channel, blocks in order (NULL: ones)
+ *   bias   [n_bias]    one per 0e channel, blocks in order (NULL: zeros)
+ * Statistics and sums are FP32; a row's statistics are formed again from x in
+ * the backward calls, nothing is kept from the forward.  A NaN or infinity in
+ * x reaches only its own block of its own row (and the weight gradients).
+ * Outputs are overwritten and must not alias inputs.  All results are bitwise
+ * reproducible (no atomics).
+ *
+ * A handle is host data only: it belongs to no device, may be used from
+ * several threads, and can be destroyed as soon as its calls have returned.
+ * The calls launch on the current device, which must own the arrays and the
+ * stream; they allocate nothing and can be captured. */
+typedef struct cgtp_norm_s* cgtp_norm;
+
+/* irreps as for cgtp_plan_create (l <= 6, multiplicities > 0, at most 32
+ * blocks, the same (l, parity) may appear again: a block of its own);
+ * eps > 0 and finite in FP32.  On failure *out is NULL.
+ * Errors: NULL, IRREPS_PARSE, LMAX, SIZE (eps, too many or too wide blocks), OOM. */
+cgtp_status cgtp_norm_create(const char* irreps, double eps, cgtp_norm* out);
+cgtp_status cgtp_norm_destroy(cgtp_norm norm); /* NULL is accepted */
+
+/* Row width D, channels (n_weight) and 0e channels (n_bias); any output
+ * pointer may be NULL.  Errors: NULL. */
+cgtp_status cgtp_norm_info(cgtp_norm norm, int64_t* d, int64_t* n_weight, int64_t* n_bias);
+
+/* y [n, D] from x [n, D] (0 <= n < 2^31).  Errors: NULL, SIZE, ALIGN, CUDA. */
+cgtp_status cgtp_norm_forward(cgtp_norm norm, int64_t n, const float* x, const float* weight,
+                              const float* bias, float* y, cgtp_stream stream);
+
+/* Bytes of device workspace that the two calls below need for n rows
+ * (256-byte aligned; nothing in it needs initialising or outlives a call).
+ * Errors: NULL, SIZE. */
+cgtp_status cgtp_norm_workspace_size(cgtp_norm norm, int64_t n, size_t* bytes);
+
+/* Gradients for grad_y [n, D] = dL/dy; with a = weight grad_y:
+ *   grad_x = r (a - c mean(a) - xh mean(a xh))
+ *   grad_weight[u] = sum_rows sum_m grad_y xh      grad_bias[u] = sum_rows grad_y
+ * Each of the three outputs may be NULL (not computed); n = 0 gives zero
+ * grad_weight and grad_bias.  The workspace is needed when grad_weight or
+ * grad_bias is given.  Errors: NULL, SIZE, ALIGN, WORKSPACE, CUDA. */
+cgtp_status cgtp_norm_backward(cgtp_norm norm, int64_t n, const float* x, const float* weight,
+                               const float* grad_y, float* grad_x, float* grad_weight, float* grad_bias,
+                               void* workspace, size_t workspace_bytes, cgtp_stream stream);
+
+/* Second order, for training on forces: the gradients of
+ *   S = <h_x, grad_x> + <h_weight, grad_weight> + <h_bias, grad_bias>
+ * over the backward above with respect to grad_y, x and weight.  With
+ * P z = z - c mean(z), J z = r (P z - xh mean(z xh)), k = h_weight grad_y,
+ * al = mean(a xh), be = mean(h_x xh), ga = mean(P(h_x) a):
+ *   gg = weight J h_x + h_weight xh + h_bias
+ *   gx = r^2 (xh (3 al be - ga) - be P a - al P h_x) + J k
+ *   gweight[u] = sum_rows sum_m grad_y J h_x
+ * Cotangents h_x [n, D], h_weight [n_weight], h_bias [n_bias] may be NULL
+ * (zero); outputs gg [n, D], gx [n, D], gweight [n_weight] may be NULL.  The
+ * workspace is needed for gweight.  Errors: NULL, SIZE, ALIGN, WORKSPACE, CUDA. */
+cgtp_status cgtp_norm_double_backward(cgtp_norm norm, int64_t n, const float* x, const float* weight,
+                                      const float* grad_y, const float* h_x, const float* h_weight,
+                                      const float* h_bias, float* gg, float* gx, float* gweight,
+                                      void* workspace, size_t workspace_bytes, cgtp_stream stream);
+
+/* ---- routing of edges to experts ------------------------------------------ */
+
+/* Gates for several gated convolutions (experts) at once: every row (an edge)
+ * has a logit per expert and is given to its k best ones.  Where the BranchIP
+ * page's router gives an edge one gate, this gives it one per expert; row e
+ * of gates is the gate array of cgtp_sparse_forward for expert e.
+ *   s = softmax(logits) or sigmoid(logits), over the row's available experts
+ *   v = s + bias                    (bias only steers the choice)
+ *   an expert is available to a row when its logit is above the lowest
+ *   float (so neither NaN nor -inf) and v is above -inf and not NaN; an
+ *   infinite logit counts as the largest float
+ *   groups: n_groups equal ranges of experts, each scored by the sum of its
+ *   group_best (1 or 2) best available v; only the top_groups best stay
+ *   ids: the k best available experts left, by v, best first
+ *   weight = scale s, or with renormalise scale s / (sum of the chosen s)
+ * The choice is made as in 64 bits whatever the size of the values (FP32 decides
+ * where its error cannot matter); of equal values the lowest index wins.
+ * Where fewer than k experts are left, the remaining ids are -1 with weight
+ * 0; a row with none left has all gates 0.
+ *
+ * The handle is host data only, as for cgtp_norm. */
+typedef struct cgtp_router_s* cgtp_router;
+
+#define CGTP_ROUTE_SOFTMAX 0
+#define CGTP_ROUTE_SIGMOID 1
+
+/* 1 <= n_experts <= 512; n_groups divides n_experts, n_groups <= 32,
+ * 1 <= top_groups <= n_groups; 1 <= k <= min(32, experts in top_groups groups);
+ * group_best 1 or 2; scale finite and > 0.  On failure *out is NULL.
+ * Errors: NULL, SIZE, OOM. */
+cgtp_status cgtp_router_create(int n_experts, int k, int score, int n_groups, int top_groups,
+                               int group_best, int renormalise, double scale, cgtp_router* out);
+cgtp_status cgtp_router_destroy(cgtp_router router); /* NULL is accepted */
+
+/* logits [n, n_experts], bias [n_experts] or NULL (device, FP32), n < 2^31 ->
+ *   ids [n, k] int32, weights [n, k]
+ *   gates [n_experts, ld]: the weight at (ids, row), 0 elsewhere; ld >= n and a
+ *     multiple of 4, so that every row is 16-byte aligned; columns from n on
+ *     are left as they were
+ *   counts [n_experts] int32: rows given to each expert
+ * Each output may be NULL (not written); the others are overwritten.  Bitwise
+ * reproducible (the only atomics add integers).  Nothing is allocated; the call
+ * can be captured.  Errors: NULL, SIZE, ALIGN, CUDA. */
+cgtp_status cgtp_router_forward(cgtp_router router, int64_t n, const float* logits, const float* bias,
+                                int32_t* ids, float* weights, float* gates, int64_t ld, int32_t* counts,
+                                cgtp_stream stream);
+
+/* Gradient of the logits [n, n_experts] (overwritten, the choice held fixed),
+ * with d_j = grad_weights[t, j] + grad_gates[ids_j, t] (either may be NULL), w
+ * the weights, p the chosen scores:
+ *   softmax renormalised:  w_j (d_j - sum d w / scale) on the chosen, else 0
+ *   softmax:               scale s_i (d_i [chosen] - sum d p)
+ *   sigmoid renormalised:  w_j (d_j - sum d w / scale) (1 - p_j) on the chosen
+ *   sigmoid:               scale d_j p_j (1 - p_j) on the chosen
+ * logits and ids as given to and by the forward; grad_weights [n, k];
+ * grad_gates [n_experts, ld], ld >= n, read only at the chosen experts.  An
+ * id outside [0, n_experts) counts as -1; of an id that a row lists twice
+ * each place counts.  Errors: NULL, SIZE, ALIGN, CUDA. */
+cgtp_status cgtp_router_backward(cgtp_router router, int64_t n, const float* logits, const int32_t* ids,
+                                 const float* grad_weights, const float* grad_gates, int64_t ld,
+                                 float* grad_logits, cgtp_stream stream);
+
 /* ---- measurement ----------------------------------------------------- */
 
 /* FP32 FMA throughput probe of the current device, the measured FP32 peak

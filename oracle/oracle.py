@@ -409,3 +409,157 @@ def sparse_backward(paths: Paths, rowptr, col, n_send: int, x, Y, W, gate, g):
     dY[act] = dYa
     dgate[act] = np.sum(W[act] * dWp, axis=1)
     return dx, dW, dY, dgate
+
+
+# ---- layer norm of irreps rows, routing of edges to experts (plain numpy)
+def _norm_blocks(irreps):
+    """(columns, channels, 0e channels or None, 2l+1) of every block."""
+    col = ch = sc = 0
+    for mul, l, p in parse_irreps(irreps):
+        d = 2 * l + 1
+        scalar = l == 0 and p > 0
+        yield slice(col, col + mul * d), slice(ch, ch + mul), slice(sc, sc + mul) if scalar else None, d
+        col, ch, sc = col + mul * d, ch + mul, sc + (mul if scalar else 0)
+
+
+def _norm_stats(x, cs, scalar, eps):
+    z = _f64(x)[:, cs]
+    mu = z.mean(1, keepdims=True) if scalar else np.zeros((len(z), 1))
+    xc = z - mu
+    r = 1.0 / np.sqrt((xc * xc).mean(1, keepdims=True) + eps)
+    return xc * r, r
+
+
+def norm_forward(irreps: str, x, weight, bias, eps: float):
+    x = _f64(x)
+    y = np.empty_like(x)
+    for cs, ws, bs, d in _norm_blocks(irreps):
+        xh, _ = _norm_stats(x, cs, bs is not None, eps)
+        y[:, cs] = xh * np.repeat(_f64(weight)[ws], d)
+        if bs is not None:
+            y[:, cs] += _f64(bias)[bs]
+    return y
+
+
+def norm_backward(irreps: str, x, weight, g, eps: float):
+    """(grad_x, grad_weight, grad_bias), from the Jacobian of each row's block:
+    d xh_i / d x_j = r (delta_ij - c/N - xh_i xh_j / N)."""
+    x, g, weight = _f64(x), _f64(g), _f64(weight)
+    dx = np.empty_like(x)
+    dw, db = np.zeros(len(weight)), []
+    for cs, ws, bs, d in _norm_blocks(irreps):
+        xh, r = _norm_stats(x, cs, bs is not None, eps)
+        n = xh.shape[1]
+        a = g[:, cs] * np.repeat(weight[ws], d)
+        dx[:, cs] = r * (a - (a.sum(1, keepdims=True) / n if bs is not None else 0.0)
+                         - xh * ((a * xh).sum(1, keepdims=True) / n))
+        dw[ws] = (g[:, cs] * xh).sum(0).reshape(-1, d).sum(1)
+        if bs is not None:
+            db.append(g[:, cs].sum(0))
+    return dx, dw, np.concatenate(db) if db else np.zeros(0)
+
+
+def norm_double_backward(irreps: str, x, weight, g, h_x, h_weight, h_bias, eps: float):
+    """(d g, dx, dweight) of S = <h_x, grad_x> + <h_weight, grad_weight> +
+    <h_bias, grad_bias>."""
+    x, g, weight, h_x, h_weight, h_bias = (_f64(t) for t in (x, g, weight, h_x, h_weight, h_bias))
+    gg, gx, gw = np.empty_like(x), np.empty_like(x), np.zeros(len(weight))
+    for cs, ws, bs, d in _norm_blocks(irreps):
+        xh, r = _norm_stats(x, cs, bs is not None, eps)
+        centre = (lambda z: z - z.mean(1, keepdims=True)) if bs is not None else (lambda z: z)
+        m = lambda z: z.mean(1, keepdims=True)
+        J = lambda z: r * (centre(z) - xh * m(z * xh))
+        wc, hc, gb, h = np.repeat(weight[ws], d), np.repeat(h_weight[ws], d), g[:, cs], h_x[:, cs]
+        a = wc * gb
+        gg[:, cs] = wc * J(h) + hc * xh + (h_bias[bs] if bs is not None else 0.0)
+        al, be, ga = m(a * xh), m(h * xh), m(centre(h) * a)
+        gx[:, cs] = r * r * (xh * (3 * al * be - ga) - be * centre(a) - al * centre(h)) + J(hc * gb)
+        gw[ws] = (gb * J(h)).sum(0).reshape(-1, d).sum(1)
+    return gg, gx, gw
+
+
+def route_forward(logits, bias, k: int, score="softmax", n_groups=1, top_groups=1, group_best=2, renormalise=True,
+                  scale=1.0):
+    """(ids, weights, gates [n_experts, rows], counts, scores) row by row."""
+    logits = _f64(logits)
+    n, E = logits.shape
+    b = np.zeros(E) if bias is None else _f64(bias)
+    ids, weights, S = np.full((n, k), -1, dtype=np.int64), np.zeros((n, k)), np.zeros((n, E))
+    low, high = float(np.finfo(np.float32).min), float(np.finfo(np.float32).max)
+    for t in range(n):
+        on = [e for e in range(E) if logits[t, e] > low]
+        l = {e: min(logits[t, e], high) for e in on}
+        if score == "softmax":
+            top = max(l.values(), default=0.0)
+            z = {e: np.exp(l[e] - top) for e in on}
+            tot = sum(z.values())
+            s = {e: z[e] / tot for e in on}
+        else:
+                s = {e: 1.0 / (1.0 + np.exp(-max(l[e], -700.0))) for e in on}
+        for e in on:
+            S[t, e] = s[e]
+        v = {e: s[e] + b[e] for e in on if s[e] + b[e] > -np.inf}
+        size = E // n_groups
+        if n_groups > 1:
+            tot = {}
+            for e in v:
+                tot.setdefault(e // size, []).append(v[e])
+            rank = sorted(tot, key=lambda q: (-sum(sorted(tot[q], reverse=True)[:group_best]), q))[:top_groups]
+            v = {e: v[e] for e in v if e // size in rank}
+        best = sorted(v, key=lambda e: (-v[e], e))[:k]
+        ids[t, :len(best)] = best
+        p = np.array([s[e] for e in best])
+        if renormalise and len(best):
+            # relative to the largest: chosen scores may all be below the smallest double
+            q = np.array([l[e] for e in best])
+            if score == "softmax":
+                p = np.exp(q - q.max())
+            else:
+                m = min(q.max(), 0.0)
+                p = np.array([np.exp(t_ - m) / (1 + np.exp(t_)) if t_ <= 0 else 1 / (1 + np.exp(-t_)) for t_ in q])
+            p = p / p.sum()
+        weights[t, :len(best)] = scale * p
+    gates, counts = np.zeros((E, n)), np.zeros(E, dtype=np.int64)
+    for t in range(n):
+        for j in range(k):
+            if ids[t, j] >= 0:
+                gates[ids[t, j], t] = weights[t, j]
+                counts[ids[t, j]] += 1
+    return ids, weights, gates, counts, S
+
+
+def route_backward(logits, ids, grad_weights, grad_gates, score="softmax", renormalise=True, scale=1.0):
+    """grad_logits [rows, n_experts] with the choice held fixed: the Jacobian
+    of the weights with respect to the scores, then of the scores."""
+    logits = _f64(logits)
+    n, E = logits.shape
+    k = ids.shape[1]
+    out = np.zeros((n, E))
+    low, high = float(np.finfo(np.float32).min), float(np.finfo(np.float32).max)
+    for t in range(n):
+        on = logits[t] > low
+        l = np.where(on, np.minimum(logits[t], high), 0.0)
+        if not on.any():
+            continue
+        if score == "softmax":
+            s = np.where(on, np.exp(l - l[on].max()), 0.0)
+            s = s / s.sum()
+        else:
+            s = np.where(on, 1.0 / (1.0 + np.exp(-l)), 0.0)
+        best = [(j, int(ids[t, j])) for j in range(k) if 0 <= ids[t, j] < E and on[ids[t, j]]]
+        d = {}
+        for j, e in best:
+            d[j] = (grad_weights[t, j] if grad_weights is not None else 0.0) + \
+                   (grad_gates[e, t] if grad_gates is not None else 0.0)
+        ds = np.zeros(E)
+        tot = sum(s[e] for _, e in best)
+        for j, e in best:
+            if not renormalise:
+                ds[e] += scale * d[j]
+            elif tot > 0:
+                ds[e] += scale * (d[j] / tot - sum(d[i] * s[q] for i, q in best) / tot ** 2)
+        if score == "softmax":  # renormalised weights do not depend on the scores' common factor: sum ds s = 0
+            out[t] = s * ds if renormalise else s * (ds - (ds * s).sum())
+        else:
+            out[t] = ds * s * (1 - s)
+    return out
