@@ -12,9 +12,16 @@
 //   gw[u] = sum_rows sum_m g J h
 // with al = mean(a xh), be = mean(h xh), ga = mean(P h a).
 //
-// One warp takes one block of one row and reads it three times (from L2 after
-// the first); the weights' gradients are a second kernel over the rows with
-// the statistics of the first.
+// Split.  The unit of work is one block of one row.  A unit of up to 4 V values
+// a thread stays in registers: a group of 1..T threads (a power of two, chosen
+// per irreps block) loads it once, forms its sums by shuffles (and, above a
+// warp, through shared memory), and writes the result, so every array moves once.
+// A CTA works for one irreps block and walks over rows, so a thread keeps the
+// same columns: the weights lie expanded to columns in shared memory, and the
+// weights' gradients add up there in slots that only their thread touches;
+// each CTA leaves one partial sum a channel, and a second launch adds these
+// (no atomics; the order is fixed by n).  Blocks wider than 16,384 values take
+// kernels that read a unit several times.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -43,41 +50,450 @@ struct NormTable {
   NormBlock b[kMaxBlocks];
 };
 
-__device__ __forceinline__ float warp_sum(float v) {
+enum { kForward = 0, kBackward = 1, kDouble = 2 };
+
+// Inputs and outputs of one call; bias is b (forward) or h_b (double).
+struct NormArgs {
+  const float *x, *w, *bias, *g, *hx, *hw;
+  float *out, *out2;  // y | grad_x | gg, gx
+};
+
+// How one irreps block is worked on in a launch.
+struct NormSeg {
+  int off, len, d, ch, sc;
+  unsigned magic;  // i / d = umulhi(i, magic); 0 for d = 1
+  int tlog, vec;   // log2 of the group's threads; 16-byte columns
+  int cta0, ncta;  // its CTAs
+  int fin0;        // its first CTA in the closing launch
+  int64_t part;    // its partial sums: [ncta][mul] of the weight, then of the bias
+};
+
+struct NormPlan {
+  int D, nseg;
+  float eps;
+  int direct;  // one CTA a block: no partial sums, the gradients are written at once
+  NormSeg s[kMaxBlocks];
+};
+
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+__device__ __forceinline__ int channel_of(int i, unsigned magic) { return magic ? (int)__umulhi(i, magic) : i; }
+
+// Sums of K values over a group of 2^tlog threads, the same bits in each of
+// them.  Above a warp: the warps' sums through red (two buffers in turn, so
+// that one barrier a call is enough), added in warp order.
+template <int K>
+__device__ __forceinline__ void group_sum(float (&v)[K], int tlog, float* red, int& turn) {
+  const int width = 1 << tlog;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < width) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    }
+  if (tlog <= 5) return;
+  const int warp = threadIdx.x >> 5, nw = width >> 5, w0 = warp & ~(nw - 1);
+  float* buf = red + turn * 32 * 8;
+  turn ^= 1;
+  if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) buf[warp * 8 + k] = v[k];
+  }
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + w0 / nw), "r"(width) : "memory");
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = buf[w0 * 8 + k];
+  for (int q = 1; q < nw; ++q) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] += buf[(w0 + q) * 8 + k];
+  }
+}
+
+// The 4 V values of this thread of one unit: with VEC, float4 v of the thread
+// is float4 v * width + lane of the unit, else value e is value e * width +
+// lane.  m of them exist; the others read as 0.
+template <int V, bool VEC>
+__device__ __forceinline__ void load_unit(const float* p, int width, int lane, int m, float (&v)[4 * V]) {
+  if (VEC) {
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (4 * q < m) t = __ldg(reinterpret_cast<const float4*>(p) + q * width + lane);
+      v[4 * q] = t.x;
+      v[4 * q + 1] = t.y;
+      v[4 * q + 2] = t.z;
+      v[4 * q + 3] = t.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4 * V; ++e) v[e] = e < m ? __ldg(p + e * width + lane) : 0.f;
+  }
+}
+
+template <int V, bool VEC>
+__device__ __forceinline__ void load_slot(const float* s, int width, int lane, int q, float (&v)[4]) {
+  if (VEC) {
+    const float4 t = reinterpret_cast<const float4*>(s)[q * width + lane];
+    v[0] = t.x;
+    v[1] = t.y;
+    v[2] = t.z;
+    v[3] = t.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = s[(4 * q + j) * width + lane];
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store_slot(float* p, int width, int lane, int q, int m, const float (&v)[4]) {
+  if (VEC) {
+    if (4 * q < m) reinterpret_cast<float4*>(p)[q * width + lane] = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (4 * q + j < m) p[(4 * q + j) * width + lane] = v[j];
+  }
+}
+
+__device__ __forceinline__ void add_slot(float4* acc, const float (&v)[4]) {
+  float4 t = *acc;
+  t.x += v[0];
+  t.y += v[1];
+  t.z += v[2];
+  t.w += v[3];
+  *acc = t;
+}
+
+// The rows of one CTA.  Shared: w (and, by the operator, bias / h_w, h_b)
+// expanded to columns; acc, acc2: the sums of the weight's and the bias's
+// gradient, slot (q, thread).
+template <int OP, int T, int V, bool VEC>
+__device__ __forceinline__ void norm_rows(const NormSeg& s, int D, float eps, int64_t n, const NormArgs& a, bool dw,
+                                          bool db, const float* sw, const float* s2, const float* s3, float4* acc,
+                                          float4* acc2, float* red) {
+  const int width = 1 << s.tlog, lane = threadIdx.x & (width - 1), groups = T >> s.tlog;
+  const int cta = blockIdx.x - s.cta0;
+  const int m = VEC ? 4 * max(0, ((s.len >> 2) - lane + width - 1) >> s.tlog)
+                    : max(0, (s.len - lane + width - 1) >> s.tlog);
+  const int64_t step = (int64_t)s.ncta * groups;
+  const float inv = 1.f / (float)s.len;
+  const bool centred = s.sc >= 0;
+  int turn = 0;
+  for (int64_t r0 = (int64_t)cta * groups; r0 < n; r0 += step) {  // the same trips for every thread of the CTA
+    const int64_t row = r0 + (threadIdx.x >> s.tlog);
+    const int mr = row < n ? m : 0;
+    const int64_t at = row * D + s.off;
+    float x[4 * V];
+    load_unit<V, VEC>(a.x + at, width, lane, mr, x);
+    float mean = 0.f;
+    if (OP == kForward) {
+      if (centred) {
+        float t[1] = {0.f};
+#pragma unroll
+        for (int e = 0; e < 4 * V; ++e) t[0] += x[e];
+        group_sum(t, s.tlog, red, turn);
+        mean = t[0] * inv;
+      }
+      float t[1] = {0.f};
+#pragma unroll
+      for (int e = 0; e < 4 * V; ++e) {
+        x[e] = e < mr ? x[e] - mean : 0.f;
+        t[0] = fmaf(x[e], x[e], t[0]);
+      }
+      group_sum(t, s.tlog, red, turn);
+      const float r = 1.f / sqrtf(fmaf(t[0], inv, eps));
+#pragma unroll
+      for (int q = 0; q < V; ++q)
+        if (4 * q < mr) {
+          float w[4], y[4];
+          load_slot<V, VEC>(sw, width, lane, q, w);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[j] = x[4 * q + j] * r * w[j];
+          if (centred) {
+            load_slot<V, VEC>(s2, width, lane, q, w);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] += w[j];
+          }
+          store_slot<VEC>(a.out + at, width, lane, q, mr, y);
+        }
+    } else if (OP == kBackward) {
+      float g[4 * V];
+      load_unit<V, VEC>(a.g + at, width, lane, mr, g);
+      float ma = 0.f;
+      if (centred) {
+        float t[2] = {0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < V; ++q)
+          if (4 * q < mr) {
+            float w[4];
+            load_slot<V, VEC>(sw, width, lane, q, w);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              t[0] += x[4 * q + j];
+              t[1] = fmaf(g[4 * q + j], w[j], t[1]);
+            }
+          }
+        group_sum(t, s.tlog, red, turn);
+        mean = t[0] * inv;
+        ma = t[1] * inv;
+      }
+      float t[2] = {0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < V; ++q)
+        if (4 * q < mr) {
+          float w[4];
+          load_slot<V, VEC>(sw, width, lane, q, w);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int e = 4 * q + j;
+            x[e] = e < mr ? x[e] - mean : 0.f;
+            t[0] = fmaf(x[e], x[e], t[0]);
+            t[1] = fmaf(g[e] * w[j], x[e], t[1]);
+          }
+        }
+      group_sum(t, s.tlog, red, turn);
+      const float r = 1.f / sqrtf(fmaf(t[0], inv, eps));
+      const float al = t[1] * inv * r;
+#pragma unroll
+      for (int q = 0; q < V; ++q)
+        if (4 * q < mr) {
+          float w[4], y[4], p[4], gq[4];
+          load_slot<V, VEC>(sw, width, lane, q, w);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int e = 4 * q + j;
+            const float xh = x[e] * r;
+            gq[j] = g[e];
+            p[j] = g[e] * xh;
+            y[j] = r * (fmaf(g[e], w[j], -ma) - xh * al);
+          }
+          if (a.out) store_slot<VEC>(a.out + at, width, lane, q, mr, y);
+          if (dw) add_slot(acc + q * T + threadIdx.x, p);
+          if (db) add_slot(acc2 + q * T + threadIdx.x, gq);
+        }
+    } else {
+      float g[4 * V], h[4 * V];
+      load_unit<V, VEC>(a.g + at, width, lane, mr, g);
+      load_unit<V, VEC>(a.hx + at, width, lane, a.hx ? mr : 0, h);
+      float ma = 0.f, mk = 0.f;
+      if (centred) {
+        float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < V; ++q)
+          if (4 * q < mr) {
+            float w[4], k[4];
+            load_slot<V, VEC>(sw, width, lane, q, w);
+            load_slot<V, VEC>(s2, width, lane, q, k);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int e = 4 * q + j;
+              t[0] += x[e];
+              t[1] = fmaf(g[e], w[j], t[1]);
+              t[2] += h[e];
+              t[3] = fmaf(g[e], k[j], t[3]);
+            }
+          }
+        group_sum(t, s.tlog, red, turn);
+        mean = t[0] * inv;
+        ma = t[1] * inv;
+        const float mh = t[2] * inv;
+        mk = t[3] * inv;
+#pragma unroll
+        for (int e = 0; e < 4 * V; ++e) h[e] = e < mr ? h[e] - mh : 0.f;
+      }
+      float t[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < V; ++q)
+        if (4 * q < mr) {
+          float w[4], k[4];
+          load_slot<V, VEC>(sw, width, lane, q, w);
+          load_slot<V, VEC>(s2, width, lane, q, k);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int e = 4 * q + j;
+            x[e] = e < mr ? x[e] - mean : 0.f;
+            const float aa = g[e] * w[j];
+            t[0] = fmaf(x[e], x[e], t[0]);
+            t[1] = fmaf(aa, x[e], t[1]);
+            t[2] = fmaf(h[e], x[e], t[2]);
+            t[3] = fmaf(g[e] * k[j], x[e], t[3]);
+            t[4] = fmaf(h[e], aa, t[4]);
+          }
+        }
+      group_sum(t, s.tlog, red, turn);
+      const float r = 1.f / sqrtf(fmaf(t[0], inv, eps));
+      const float al = t[1] * inv * r, be = t[2] * inv * r, de = t[3] * inv * r, ga = t[4] * inv;
+      const float cx = 3.f * al * be - ga;
+#pragma unroll
+      for (int q = 0; q < V; ++q)
+        if (4 * q < mr) {
+          float w[4], k[4], b[4] = {0.f, 0.f, 0.f, 0.f}, y[4], z[4], p[4];
+          load_slot<V, VEC>(sw, width, lane, q, w);
+          load_slot<V, VEC>(s2, width, lane, q, k);
+          if (centred) load_slot<V, VEC>(s3, width, lane, q, b);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int e = 4 * q + j;
+            const float xh = x[e] * r, jh = r * (h[e] - xh * be);
+            y[j] = fmaf(w[j], jh, fmaf(k[j], xh, b[j]));
+            z[j] = r * (r * (xh * cx - be * fmaf(g[e], w[j], -ma) - al * h[e]) + (fmaf(g[e], k[j], -mk) - xh * de));
+            p[j] = g[e] * jh;
+          }
+          if (a.out) store_slot<VEC>(a.out + at, width, lane, q, mr, y);
+          if (a.out2) store_slot<VEC>(a.out2 + at, width, lane, q, mr, z);
+          if (dw) add_slot(acc + q * T + threadIdx.x, p);
+        }
+    }
+  }
+}
+
+// Shared floats of one CTA: the expanded parameters of a block of `len` values
+// (each padded to whole slots of its group), the accumulators, the sums.
+constexpr int kRed = 2 * 32 * 8;
+__host__ __device__ constexpr int expanded_arrays(int op, bool centred) {
+  return 1 + (op == kForward && centred) + (op == kDouble) + (op == kDouble && centred);
+}
+__host__ __device__ inline int expanded(int len, int tlog) {
+  const int slot = 4 << tlog;  // a group's values of one slot
+  return (len + slot - 1) / slot * slot;
+}
+
+template <int OP, int T, int V, int MIN>
+__global__ void __launch_bounds__(T, MIN) norm_kernel(const __grid_constant__ NormPlan p, int64_t n,
+                                                      const __grid_constant__ NormArgs a, float* __restrict__ part,
+                                                      float* __restrict__ dw, float* __restrict__ db) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  extern __shared__ float4 smem4[];
+  float* smem = reinterpret_cast<float*>(smem4);
+  int q = 0;
+  while (q + 1 < p.nseg && (int)blockIdx.x >= p.s[q + 1].cta0) ++q;
+  const NormSeg s = p.s[q];
+  const int size = expanded(s.len, s.tlog);
+  float* sw = smem;
+  const bool centred = s.sc >= 0;
+  float* s2 = sw + size;  // forward: bias of a centred block; double: h_w
+  float* s3 = s2 + size;  // double: h_b of a centred block
+  float4* acc = reinterpret_cast<float4*>(smem + expanded_arrays(OP, centred) * size);
+  const bool want_w = OP != kForward && dw, want_b = OP == kBackward && db && centred;
+  float4* acc2 = acc + (want_w ? T * V : 0);
+  float* red = reinterpret_cast<float*>(acc2 + (want_b ? T * V : 0));
+  for (int i = threadIdx.x; i < size; i += T) {
+    const int c = channel_of(i, s.magic);
+    const bool in = i < s.len;
+    sw[i] = !in ? 0.f : a.w ? __ldg(a.w + s.ch + c) : 1.f;
+    if (OP == kForward && centred) s2[i] = in && a.bias ? __ldg(a.bias + s.sc + c) : 0.f;
+    if (OP == kDouble) s2[i] = in && a.hw ? __ldg(a.hw + s.ch + c) : 0.f;
+    if (OP == kDouble && centred) s3[i] = in && a.bias ? __ldg(a.bias + s.sc + c) : 0.f;
+  }
+  if (OP != kForward) {
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = threadIdx.x; i < (want_w ? T * V : 0) + (want_b ? T * V : 0); i += T) acc[i] = zero;
+  }
+  __syncthreads();
+  if (s.vec)
+    norm_rows<OP, T, V, true>(s, p.D, p.eps, n, a, want_w, want_b, sw, s2, s3, acc, acc2, red);
+  else
+    norm_rows<OP, T, V, false>(s, p.D, p.eps, n, a, want_w, want_b, sw, s2, s3, acc, acc2, red);
+  if (OP == kForward || (!want_w && !want_b)) return;
+  // this CTA's sums: over its groups and over a channel's components
+  __syncthreads();
+  const int mul = s.len / s.d, width = 1 << s.tlog, groups = T >> s.tlog, cta = blockIdx.x - s.cta0;
+  for (int c = threadIdx.x; c < mul; c += T) {
+    float v = 0.f, b = 0.f;
+    for (int k = 0; k < s.d; ++k) {
+      const int i = c * s.d + k;
+      const int e = s.vec ? (i >> 2 >> s.tlog) * 4 + (i & 3) : i >> s.tlog;
+      const int lane = s.vec ? (i >> 2) & (width - 1) : i & (width - 1);
+      const int at = ((e >> 2) * T + lane) * 4 + (e & 3);
+      for (int u = 0; u < groups; ++u) {
+        if (want_w) v += reinterpret_cast<float*>(acc)[at + u * width * 4];
+        if (want_b) b += reinterpret_cast<float*>(acc2)[at + u * width * 4];
+      }
+    }
+    if (p.direct) {
+      if (want_w) dw[s.ch + c] = v;
+      if (want_b) db[s.sc + c] = b;
+    } else {
+      if (want_w) part[s.part + (int64_t)cta * mul + c] = v;
+      if (want_b) part[s.part + (int64_t)(s.ncta + cta) * mul + c] = b;
+    }
+  }
+}
+
+// The closing sums: a CTA takes 32 channels of one block; eight warps share
+// the CTAs' partial sums, which are then added in warp order.
+__global__ void __launch_bounds__(256) norm_finish_kernel(const __grid_constant__ NormPlan p,
+                                                          const float* __restrict__ part, float* __restrict__ dw,
+                                                          float* __restrict__ db) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  int q = 0;
+  while (q + 1 < p.nseg && (int)blockIdx.x >= p.s[q + 1].fin0) ++q;
+  const NormSeg s = p.s[q];
+  const int mul = s.len / s.d, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tiles = (mul + 31) / 32, tile = blockIdx.x - s.fin0;
+  const bool bias = tile >= tiles;
+  const int c = (bias ? tile - tiles : tile) * 32 + lane;
+  float* out = bias ? (db ? db + s.sc : nullptr) : (dw ? dw + s.ch : nullptr);
+  if (!out) return;
+  float v = 0.f;
+  if (c < mul) {
+    const float* src = part + s.part + (bias ? (int64_t)s.ncta * mul : 0) + c;
+#pragma unroll 4
+    for (int k = warp; k < s.ncta; k += 8) v += src[(int64_t)k * mul];
+  }
+  __shared__ float sums[8][32];
+  sums[warp][lane] = v;
+  __syncthreads();
+  if (warp == 0 && c < mul) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) v += sums[k][lane];
+    out[c] = v;
+  }
+}
+
+// ---- blocks wider than the registers of a CTA: one CTA a unit, several reads
+
+constexpr int kWide = 256;
+
+__device__ __forceinline__ float cta_sum(float v, float* red, int& turn) {
+  float t[1] = {v};
+  group_sum(t, 8, red, turn);
+  return t[0];
 }
 
 // mean (0 unless centred) and 1 / sqrt(variance + eps) of one block
-__device__ __forceinline__ void block_stats(const float* x, const NormBlock& b, float eps, int lane, float* mu,
-                                            float* r) {
+__device__ __forceinline__ void block_stats(const float* x, const NormBlock& b, float eps, float* red, int& turn,
+                                            float* mu, float* r) {
   const float inv = 1.f / (float)b.len;
   float m = 0.f;
   if (b.sc >= 0) {
-    for (int i = lane; i < b.len; i += 32) m += x[i];
-    m = warp_sum(m) * inv;
+    for (int i = threadIdx.x; i < b.len; i += kWide) m += x[i];
+    m = cta_sum(m, red, turn) * inv;
   }
   float v = 0.f;
-  for (int i = lane; i < b.len; i += 32) {
+  for (int i = threadIdx.x; i < b.len; i += kWide) {
     const float t = x[i] - m;
     v = fmaf(t, t, v);
   }
   *mu = m;
-  *r = 1.f / sqrtf(warp_sum(v) * inv + eps);
+  *r = 1.f / sqrtf(cta_sum(v, red, turn) * inv + eps);
 }
 
-__global__ void __launch_bounds__(256) norm_forward_kernel(const __grid_constant__ NormTable t, int64_t n,
-                                                           const float* __restrict__ x, const float* __restrict__ w,
-                                                           const float* __restrict__ bias, float* __restrict__ y) {
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * 8;
-  for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < n * t.nblocks; u += warps) {
+__global__ void __launch_bounds__(kWide) wide_forward_kernel(const __grid_constant__ NormTable t, int64_t n,
+                                                             const float* __restrict__ x, const float* __restrict__ w,
+                                                             const float* __restrict__ bias, float* __restrict__ y) {
+  __shared__ float red[kRed];
+  int turn = 0;
+  for (int64_t u = blockIdx.x; u < n * t.nblocks; u += gridDim.x) {
     const NormBlock b = t.b[u % t.nblocks];
     const int64_t at = u / t.nblocks * t.D + b.off;
     float mu, r;
-    block_stats(x + at, b, t.eps, lane, &mu, &r);
-    for (int i = lane; i < b.len; i += 32) {
+    block_stats(x + at, b, t.eps, red, turn, &mu, &r);
+    for (int i = threadIdx.x; i < b.len; i += kWide) {
       const int c = i / b.d;
       const float v = (x[at + i] - mu) * r * (w ? w[b.ch + c] : 1.f);
       y[at + i] = b.sc >= 0 && bias ? v + bias[b.sc + c] : v;
@@ -86,63 +502,63 @@ __global__ void __launch_bounds__(256) norm_forward_kernel(const __grid_constant
 }
 
 // stats[u] = (mu, r, mean(h) if centred, mean(h xh)) of unit u = row * nblocks + block
-__global__ void __launch_bounds__(256) norm_backward_kernel(const __grid_constant__ NormTable t, int64_t n,
-                                                            const float* __restrict__ x, const float* __restrict__ w,
-                                                            const float* __restrict__ g, float* __restrict__ dx,
-                                                            float4* __restrict__ stats) {
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * 8;
-  for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < n * t.nblocks; u += warps) {
+__global__ void __launch_bounds__(kWide) wide_backward_kernel(const __grid_constant__ NormTable t, int64_t n,
+                                                              const float* __restrict__ x, const float* __restrict__ w,
+                                                              const float* __restrict__ g, float* __restrict__ dx,
+                                                              float4* __restrict__ stats) {
+  __shared__ float red[kRed];
+  int turn = 0;
+  for (int64_t u = blockIdx.x; u < n * t.nblocks; u += gridDim.x) {
     const NormBlock b = t.b[u % t.nblocks];
     const int64_t at = u / t.nblocks * t.D + b.off;
     float mu, r;
-    block_stats(x + at, b, t.eps, lane, &mu, &r);
-    if (lane == 0 && stats) stats[u] = make_float4(mu, r, 0.f, 0.f);
+    block_stats(x + at, b, t.eps, red, turn, &mu, &r);
+    if (threadIdx.x == 0 && stats) stats[u] = make_float4(mu, r, 0.f, 0.f);
     if (!dx) continue;
     float sa = 0.f, sax = 0.f;
-    for (int i = lane; i < b.len; i += 32) {
+    for (int i = threadIdx.x; i < b.len; i += kWide) {
       const float a = g[at + i] * (w ? w[b.ch + i / b.d] : 1.f);
       sa += a;
       sax = fmaf(a, (x[at + i] - mu) * r, sax);
     }
     const float inv = 1.f / (float)b.len;
-    const float ma = b.sc >= 0 ? warp_sum(sa) * inv : 0.f;
-    const float al = warp_sum(sax) * inv;
-    for (int i = lane; i < b.len; i += 32) {
+    const float ma = b.sc >= 0 ? cta_sum(sa, red, turn) * inv : 0.f;
+    const float al = cta_sum(sax, red, turn) * inv;
+    for (int i = threadIdx.x; i < b.len; i += kWide) {
       const float a = g[at + i] * (w ? w[b.ch + i / b.d] : 1.f);
       dx[at + i] = r * (a - ma - (x[at + i] - mu) * r * al);
     }
   }
 }
 
-__global__ void __launch_bounds__(256) norm_double_kernel(const __grid_constant__ NormTable t, int64_t n,
-                                                          const float* __restrict__ x, const float* __restrict__ w,
-                                                          const float* __restrict__ g, const float* __restrict__ hx,
-                                                          const float* __restrict__ hw, const float* __restrict__ hb,
-                                                          float* __restrict__ gg, float* __restrict__ gx,
-                                                          float4* __restrict__ stats) {
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * 8;
-  for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < n * t.nblocks; u += warps) {
+__global__ void __launch_bounds__(kWide) wide_double_kernel(const __grid_constant__ NormTable t, int64_t n,
+                                                            const float* __restrict__ x, const float* __restrict__ w,
+                                                            const float* __restrict__ g, const float* __restrict__ hx,
+                                                            const float* __restrict__ hw, const float* __restrict__ hb,
+                                                            float* __restrict__ gg, float* __restrict__ gx,
+                                                            float4* __restrict__ stats) {
+  __shared__ float red[kRed];
+  int turn = 0;
+  for (int64_t u = blockIdx.x; u < n * t.nblocks; u += gridDim.x) {
     const NormBlock b = t.b[u % t.nblocks];
     const int64_t at = u / t.nblocks * t.D + b.off;
     const float inv = 1.f / (float)b.len;
     float mu, r;
-    block_stats(x + at, b, t.eps, lane, &mu, &r);
+    block_stats(x + at, b, t.eps, red, turn, &mu, &r);
     float sa = 0.f, sh = 0.f, sk = 0.f;
     if (b.sc >= 0) {
-      for (int i = lane; i < b.len; i += 32) {
+      for (int i = threadIdx.x; i < b.len; i += kWide) {
         const int c = b.ch + i / b.d;
         sa = fmaf(g[at + i], w ? w[c] : 1.f, sa);
         if (hx) sh += hx[at + i];
         if (hw) sk = fmaf(g[at + i], hw[c], sk);
       }
-      sa = warp_sum(sa) * inv;
-      sh = warp_sum(sh) * inv;
-      sk = warp_sum(sk) * inv;
+      sa = cta_sum(sa, red, turn) * inv;
+      sh = cta_sum(sh, red, turn) * inv;
+      sk = cta_sum(sk, red, turn) * inv;
     }
     float sax = 0.f, shx = 0.f, skx = 0.f, sha = 0.f;
-    for (int i = lane; i < b.len; i += 32) {
+    for (int i = threadIdx.x; i < b.len; i += kWide) {
       const int c = b.ch + i / b.d;
       const float xh = (x[at + i] - mu) * r, gi = g[at + i];
       const float a = gi * (w ? w[c] : 1.f), h = hx ? hx[at + i] - sh : 0.f;
@@ -151,11 +567,11 @@ __global__ void __launch_bounds__(256) norm_double_kernel(const __grid_constant_
       sha = fmaf(h, a, sha);
       if (hw) skx = fmaf(gi * hw[c], xh, skx);
     }
-    const float al = warp_sum(sax) * inv, be = warp_sum(shx) * inv, ga = warp_sum(sha) * inv,
-                de = warp_sum(skx) * inv;
-    if (lane == 0 && stats) stats[u] = make_float4(mu, r, sh, be);
+    const float al = cta_sum(sax, red, turn) * inv, be = cta_sum(shx, red, turn) * inv,
+                ga = cta_sum(sha, red, turn) * inv, de = cta_sum(skx, red, turn) * inv;
+    if (threadIdx.x == 0 && stats) stats[u] = make_float4(mu, r, sh, be);
     const float cx = 3.f * al * be - ga;
-    for (int i = lane; i < b.len; i += 32) {
+    for (int i = threadIdx.x; i < b.len; i += kWide) {
       const int c = b.ch + i / b.d;
       const float xh = (x[at + i] - mu) * r, gi = g[at + i], wi = w ? w[c] : 1.f, hwi = hw ? hw[c] : 0.f;
       const float h = hx ? hx[at + i] - sh : 0.f;
@@ -170,20 +586,22 @@ __global__ void __launch_bounds__(256) norm_double_kernel(const __grid_constant_
   }
 }
 
-// One CTA per channel: the sums over rows and components of g xh (h null) or
-// g J h, and of g for 0e channels.  stats as written above.
-__global__ void __launch_bounds__(256) norm_weight_kernel(const __grid_constant__ NormTable t, int64_t n,
-                                                          const float* __restrict__ x, const float* __restrict__ g,
-                                                          const float* __restrict__ hx, bool second,
-                                                          const float4* __restrict__ stats, float* __restrict__ dw,
-                                                          float* __restrict__ db) {
+// One CTA per channel: the sums over rows and components of g xh or g J h, and
+// of g for 0e channels.  stats as written above.
+__global__ void __launch_bounds__(kWide) wide_weight_kernel(const __grid_constant__ NormTable t, int64_t n,
+                                                            const float* __restrict__ x, const float* __restrict__ g,
+                                                            const float* __restrict__ hx, bool second,
+                                                            const float4* __restrict__ stats, float* __restrict__ dw,
+                                                            float* __restrict__ db) {
+  __shared__ float red[kRed];
+  int turn = 0;
   const int ch = blockIdx.x;
   int q = 0;
   while (q + 1 < t.nblocks && t.b[q + 1].ch <= ch) ++q;
   const NormBlock b = t.b[q];
   const int c = ch - b.ch;
   float sw = 0.f, sb = 0.f;
-  for (int64_t i = threadIdx.x; i < n * b.d; i += 256) {
+  for (int64_t i = threadIdx.x; i < n * b.d; i += kWide) {
     const int64_t row = i / b.d, at = row * t.D + b.off + c * b.d + (i - row * b.d);
     const float4 s = stats[row * t.nblocks + q];
     const float xh = (x[at] - s.x) * s.y;
@@ -191,20 +609,9 @@ __global__ void __launch_bounds__(256) norm_weight_kernel(const __grid_constant_
     sw = fmaf(g[at], v, sw);
     sb += g[at];
   }
-  __shared__ float part[2][8];
-  sw = warp_sum(sw);
-  sb = warp_sum(sb);
-  if ((threadIdx.x & 31) == 0) {
-    part[0][threadIdx.x >> 5] = sw;
-    part[1][threadIdx.x >> 5] = sb;
-  }
-  __syncthreads();
+  sw = cta_sum(sw, red, turn);
+  sb = cta_sum(sb, red, turn);
   if (threadIdx.x == 0) {
-    sw = sb = 0.f;
-    for (int k = 0; k < 8; ++k) {
-      sw += part[0][k];
-      sb += part[1][k];
-    }
     if (dw) dw[ch] = sw;
     if (db && b.sc >= 0) db[b.sc + c] = sb;
   }
@@ -224,7 +631,77 @@ cgtp_status norm_aligned(std::initializer_list<const void*> ps) {
   return CGTP_OK;
 }
 
-size_t norm_workspace(const NormTable& t, int64_t n) { return ((size_t)n * t.nblocks * sizeof(float4) + 255) & ~size_t(255); }
+constexpr int kSms = 148;
+constexpr int kNarrow = 4096;    // values a group of 256 threads holds, 16 a thread
+constexpr int kMiddle = 16384;   // values a group of 512 threads holds, 32 a thread
+constexpr size_t kMaxShared = 227 * 1024;
+
+int widest(const NormTable& t) {
+  int m = 0;
+  for (int q = 0; q < t.nblocks; ++q) m = std::max(m, t.b[q].len);
+  return m;
+}
+
+// CTAs of a launch: as many as are resident (the backward operators keep sums
+// per CTA), twice that for the forward.
+int target_ctas(int op, bool narrow) { return kSms * (narrow ? (op == kForward ? 12 : 4) : (op == kForward ? 4 : 1)); }
+
+// The division of n rows among the CTAs; *floats: the partial sums' size,
+// *shared: bytes of shared memory.  False where some block does not fit a
+// CTA's registers or shared memory (the kernels for wide blocks run then).
+bool norm_plan(const NormTable& t, int op, int64_t n, NormPlan& p, int64_t* floats, size_t* shared) {
+  const int wide = widest(t);
+  if (wide > kMiddle) return false;
+  const bool narrow = wide <= kNarrow;
+  const int T = narrow ? 256 : 512, V = narrow ? 4 : 8;
+  p.D = t.D;
+  p.nseg = t.nblocks;
+  p.eps = t.eps;
+  p.direct = 1;
+  int cta = 0, fin = 0;
+  int64_t part = 0;
+  size_t most = 0;
+  for (int q = 0; q < t.nblocks; ++q) {
+    const NormBlock& b = t.b[q];
+    NormSeg& s = p.s[q];
+    s.off = b.off;
+    s.len = b.len;
+    s.d = b.d;
+    s.ch = b.ch;
+    s.sc = b.sc;
+    s.magic = b.d == 1 ? 0u : (unsigned)((uint64_t(1) << 32) / b.d + 1);
+    s.vec = t.D % 4 == 0 && b.off % 4 == 0 && b.len % 4 == 0;
+    s.tlog = 0;
+    while ((4 * V << s.tlog) < b.len) ++s.tlog;
+    const int64_t groups = T >> s.tlog, need = (n + groups - 1) / groups;
+    const int64_t share = ((int64_t)target_ctas(op, narrow) * b.len + t.D - 1) / t.D;
+    s.ncta = (int)std::max<int64_t>(1, std::min(need, share));
+    s.cta0 = cta;
+    cta += s.ncta;
+    s.fin0 = fin;
+    const int mul = b.len / b.d, tiles = (mul + 31) / 32;
+    fin += tiles * (op == kBackward && b.sc >= 0 ? 2 : 1);
+    s.part = part;
+    part += (int64_t)s.ncta * mul * (op == kBackward && b.sc >= 0 ? 2 : 1);
+    if (s.ncta > 1) p.direct = 0;
+    size_t floats_here = (size_t)expanded_arrays(op, b.sc >= 0) * expanded(b.len, s.tlog) + kRed;
+    if (op != kForward) floats_here += (size_t)4 * T * V * (op == kBackward && b.sc >= 0 ? 2 : 1);
+    most = std::max(most, floats_here * sizeof(float));
+  }
+  *floats = part;
+  *shared = most;
+  return most <= kMaxShared;
+}
+
+size_t norm_workspace(const NormTable& t, int64_t n) {
+  int64_t bytes = 0, floats;
+  size_t shared;
+  NormPlan p;
+  for (int op : {kBackward, kDouble})
+    bytes = std::max(bytes, norm_plan(t, op, n, p, &floats, &shared) ? floats * (int64_t)sizeof(float)
+                                                                     : n * t.nblocks * (int64_t)sizeof(float4));
+  return ((size_t)bytes + 255) & ~size_t(255);
+}
 
 cgtp_status norm_workspace_check(const NormTable& t, int64_t n, const void* ws, size_t bytes) {
   const size_t need = norm_workspace(t, n);
@@ -233,8 +710,62 @@ cgtp_status norm_workspace_check(const NormTable& t, int64_t n, const void* ws, 
   return CGTP_OK;
 }
 
-unsigned unit_grid(const NormTable& t, int64_t n) {
-  return (unsigned)std::min<int64_t>((n * t.nblocks + 7) / 8, 148 * 8);
+template <class... KArgs, class... Args>
+cudaError_t launch_dependent(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t shared, cudaStream_t s,
+                             Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = shared;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+template <int OP, int T, int V, int MIN>
+cudaError_t launch_rows(const NormPlan& p, int64_t n, const NormArgs& a, size_t shared, float* dw, float* db,
+                        float* part, cudaStream_t s) {
+  auto kernel = norm_kernel<OP, T, V, MIN>;
+  if (shared > 48 * 1024) {
+    // always the same value: threads with other sizes do not undo it
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxShared);
+    if (e != cudaSuccess) return e;
+  }
+  const NormSeg& last = p.s[p.nseg - 1];
+  return launch_dependent(kernel, (unsigned)(last.cta0 + last.ncta), T, shared, s, p, n, a, part, dw, db);
+}
+
+template <int OP>
+cudaError_t launch_norm(const NormTable& t, int64_t n, const NormArgs& a, float* dw, float* db, void* workspace,
+                        cudaStream_t s) {
+  NormPlan p;
+  int64_t floats;
+  size_t shared;
+  if (!norm_plan(t, OP, n, p, &floats, &shared)) {
+    float4* stats = (float4*)workspace;
+    const unsigned grid = (unsigned)std::min<int64_t>(n * t.nblocks, kSms * 8);
+    if (OP == kForward) wide_forward_kernel<<<grid, kWide, 0, s>>>(t, n, a.x, a.w, a.bias, a.out);
+    if (OP == kBackward) wide_backward_kernel<<<grid, kWide, 0, s>>>(t, n, a.x, a.w, a.g, a.out, stats);
+    if (OP == kDouble)
+      wide_double_kernel<<<grid, kWide, 0, s>>>(t, n, a.x, a.w, a.g, a.hx, a.hw, a.bias, a.out, a.out2, stats);
+    if (stats)
+      wide_weight_kernel<<<(unsigned)t.C, kWide, 0, s>>>(t, n, a.x, a.g, a.hx, OP == kDouble, stats, dw, db);
+    return cudaGetLastError();
+  }
+  float* part = (float*)workspace;
+  const cudaError_t e =
+      widest(t) <= kNarrow
+          ? launch_rows<OP, 256, 4, OP == kForward ? 4 : OP == kBackward ? 3 : 2>(p, n, a, shared, dw, db, part, s)
+          : launch_rows<OP, 512, 8, OP == kForward ? 2 : 1>(p, n, a, shared, dw, db, part, s);
+  if (e != cudaSuccess || (!dw && !db) || p.direct) return e;
+  int fin = 0;
+  for (int q = 0; q < t.nblocks; ++q)
+    fin += (t.b[q].len / t.b[q].d + 31) / 32 * (OP == kBackward && t.b[q].sc >= 0 ? 2 : 1);
+  return launch_dependent(norm_finish_kernel, (unsigned)fin, 256, 0, s, p, (const float*)part, dw, db);
 }
 
 }  // namespace
@@ -309,8 +840,8 @@ cgtp_status cgtp_norm_forward(cgtp_norm norm, int64_t n, const float* x, const f
   if (n == 0) return CGTP_OK;
   if (!x || !y) return fail(CGTP_ERR_NULL, "x or y is NULL");
   if ((st = norm_aligned({x, weight, bias, y})) != CGTP_OK) return st;
-  norm_forward_kernel<<<unit_grid(norm->t, n), 256, 0, (cudaStream_t)stream>>>(norm->t, n, x, weight, bias, y);
-  CGTP_CUDA_TRY(cudaGetLastError());
+  CGTP_CUDA_TRY(launch_norm<kForward>(norm->t, n, {x, weight, bias, nullptr, nullptr, nullptr, y, nullptr},
+                                      nullptr, nullptr, nullptr, (cudaStream_t)stream));
   return CGTP_OK;
 }
 
@@ -341,11 +872,8 @@ cgtp_status cgtp_norm_backward(cgtp_norm norm, int64_t n, const float* x, const 
   }
   if (!params && !grad_x) return CGTP_OK;
   if (params && (st = norm_workspace_check(t, n, workspace, workspace_bytes)) != CGTP_OK) return st;
-  float4* stats = params ? (float4*)workspace : nullptr;
-  norm_backward_kernel<<<unit_grid(t, n), 256, 0, s>>>(t, n, x, weight, grad_y, grad_x, stats);
-  if (params)
-    norm_weight_kernel<<<(unsigned)t.C, 256, 0, s>>>(t, n, x, grad_y, nullptr, false, stats, grad_weight, grad_bias);
-  CGTP_CUDA_TRY(cudaGetLastError());
+  CGTP_CUDA_TRY(launch_norm<kBackward>(t, n, {x, weight, nullptr, grad_y, nullptr, nullptr, grad_x, nullptr},
+                                       grad_weight, grad_bias, params ? workspace : nullptr, s));
   return CGTP_OK;
 }
 
@@ -366,11 +894,8 @@ cgtp_status cgtp_norm_double_backward(cgtp_norm norm, int64_t n, const float* x,
   }
   if (!gg && !gx && !gweight) return CGTP_OK;
   if (gweight && (st = norm_workspace_check(t, n, workspace, workspace_bytes)) != CGTP_OK) return st;
-  float4* stats = gweight ? (float4*)workspace : nullptr;
-  norm_double_kernel<<<unit_grid(t, n), 256, 0, s>>>(t, n, x, weight, grad_y, h_x, h_weight, h_bias, gg, gx, stats);
-  if (gweight)
-    norm_weight_kernel<<<(unsigned)t.C, 256, 0, s>>>(t, n, x, grad_y, h_x, true, stats, gweight, nullptr);
-  CGTP_CUDA_TRY(cudaGetLastError());
+  CGTP_CUDA_TRY(launch_norm<kDouble>(t, n, {x, weight, h_bias, grad_y, h_x, h_weight, gg, gx}, gweight, nullptr,
+                                     gweight ? workspace : nullptr, s));
   return CGTP_OK;
 }
 
