@@ -426,7 +426,8 @@ cgtp_status cgtp_norm_double_backward(cgtp_norm norm, int64_t n, const float* x,
  *   ids: the k best available experts left, by v, best first
  *   weight = scale s, or with renormalise scale s / (sum of the chosen s)
  * The choice is made as in 64 bits whatever the size of the values (FP32 decides
- * where its error cannot matter); of equal values the lowest index wins.
+ * where its error cannot matter); without a bias and groups it goes by the
+ * logits, whose order is the scores'.  Of equal values the lowest index wins.
  * Where fewer than k experts are left, the remaining ids are -1 with weight
  * 0; a row with none left has all gates 0.
  *

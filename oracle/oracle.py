@@ -499,6 +499,8 @@ def route_forward(logits, bias, k: int, score="softmax", n_groups=1, top_groups=
         for e in on:
             S[t, e] = s[e]
         v = {e: s[e] + b[e] for e in on if s[e] + b[e] > -np.inf}
+        if bias is None and n_groups == 1:
+            v = l  # the scores' order, also where 64 bits no longer tell them apart
         size = E // n_groups
         if n_groups > 1:
             tot = {}
