@@ -9,6 +9,7 @@ fallback: if the library is missing this module raises on import.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -106,31 +107,44 @@ def _require_device(t, name, dev):
         raise ValueError(f"{name}: on {t.device}, the other arguments on {dev}")
 
 
+@functools.lru_cache(None)
+def _torch():
+    import torch
+    return torch
+
+
+@functools.lru_cache(None)
+def _types():
+    return {"f32": _torch().float32, "i32": _torch().int32}
+
+
 def _args(dev, *specs):
     """Device pointers of tensor arguments, each spec (tensor, name, count,
     kind), after the checks that keep the kernels' flat indexing inside
     them: first dtype (kind "f32" or "i32") and exactly `count` elements for
     every argument, then a contiguous CUDA tensor on `dev`.  None passes as
     NULL (the library then reports a required argument as CGTP_ERR_NULL)."""
-    import torch
+    types = _types()
     for t, name, count, kind in specs:
-        if t is None:
-            continue
-        want = torch.float32 if kind == "f32" else torch.int32
-        if t.dtype != want:
-            raise TypeError(f"{name}: expected {want}, got {t.dtype}")
-        if t.numel() != count:
-            raise ValueError(f"{name}: expected {count} elements, got shape {tuple(t.shape)}")
+        if t is not None:
+            if t.dtype is not types[kind]:
+                raise TypeError(f"{name}: expected {types[kind]}, got {t.dtype}")
+            if t.numel() != count:
+                raise ValueError(f"{name}: expected {count} elements, got shape {tuple(t.shape)}")
+    ptrs = []
     for t, name, _, _ in specs:
         if t is not None:
-            _require_device(t, name, dev)
-    return [None if t is None else ctypes.c_void_p(t.data_ptr()) for t, _, _, _ in specs]
+            if not t.is_cuda or not t.is_contiguous() or (dev is not None and t.device != dev):
+                _require_device(t, name, dev)
+            t = t.data_ptr()
+        ptrs.append(t)
+    return ptrs
 
 
 def _workspace(t, dev):
     """Pointer and byte size of a caller workspace (any dtype)."""
     _require_device(t, "workspace", dev)
-    return ctypes.c_void_p(t.data_ptr()), t.numel() * t.element_size()
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def _stream(stream=None):
@@ -139,15 +153,17 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _on_current(dev, stream):
-    """The calls of handles that belong to no device launch on the current
-    one: refuse arrays or a stream of another."""
-    import torch
-    if dev.type == "cuda":
-        if dev.index != torch.cuda.current_device():
-            raise ValueError(f"the arrays are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"the arrays are on {dev}, the stream is on {stream.device}")
+def _stream_of(dev, stream):
+    """The stream's handle for calls of handles that belong to no device: they
+    launch on the current one, so arrays or a stream of another are refused."""
+    torch = _torch()
+    if dev.index != torch._C._cuda_getDevice():
+        raise ValueError(f"the arrays are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+    if stream.device != dev:
+        raise ValueError(f"the arrays are on {dev}, the stream is on {stream.device}")
+    return stream.cuda_stream
 
 
 def real_cg(l1: int, l2: int, l3: int) -> np.ndarray:
@@ -513,15 +529,22 @@ class LayerNorm:
         except Exception:
             pass
 
+    def _new(self, x, *shape):
+        return x.new_empty(shape) if x.dtype is _types()["f32"] else x.new_empty(shape, dtype=_types()["f32"])
+
+    def _like(self, x, n):
+        """A new [n, D] array for x (empty_like is the cheaper call)."""
+        if x.dim() == 2 and x.dtype is _types()["f32"] and x.is_contiguous() and x.shape[1] == self.d:
+            return _torch().empty_like(x)
+        return self._new(x, n, self.d)
+
     def forward(self, x, weight=None, bias=None, out=None, stream=None):
-        import torch
         n, dev = x.shape[0], x.device
         if out is None:
-            out = torch.empty((n, self.d), dtype=torch.float32, device=dev)
+            out = self._like(x, n)
         ptrs = _args(dev, (x, "x", n * self.d, "f32"), (weight, "weight", self.n_weight, "f32"),
                      (bias, "bias", self.n_bias, "f32"), (out, "out", n * self.d, "f32"))
-        _on_current(dev, stream)
-        _check(_lib.cgtp_norm_forward(self._h, n, *ptrs, _stream(stream)))
+        _check(_lib.cgtp_norm_forward(self._h, n, *ptrs, _stream_of(dev, stream)))
         return out
 
     def workspace_size(self, n: int) -> int:
@@ -538,18 +561,15 @@ class LayerNorm:
     def backward(self, x, weight, grad_out, want=("x", "weight", "bias"), grads=None, workspace=None,
                  stream=None):
         """(grad_x, grad_weight, grad_bias) for grad_out = dL/dy."""
-        import torch
         n, dev = x.shape[0], x.device
         if grads is None:
-            f = lambda *shape: torch.empty(shape, dtype=torch.float32, device=dev)
-            grads = (f(n, self.d) if "x" in want else None, f(self.n_weight) if "weight" in want else None,
-                     f(self.n_bias) if "bias" in want else None)
+            grads = (self._like(x, n) if "x" in want else None, self._new(x, self.n_weight) if "weight" in want else None,
+                     self._new(x, self.n_bias) if "bias" in want else None)
         dx, dw, db = grads
         ptrs = _args(dev, (x, "x", n * self.d, "f32"), (weight, "weight", self.n_weight, "f32"),
                      (grad_out, "grad_out", n * self.d, "f32"), (dx, "grad_x", n * self.d, "f32"),
                      (dw, "grad_weight", self.n_weight, "f32"), (db, "grad_bias", self.n_bias, "f32"))
-        _on_current(dev, stream)
-        _check(_lib.cgtp_norm_backward(self._h, n, *ptrs, *self._ws(workspace, n, dev), _stream(stream)))
+        _check(_lib.cgtp_norm_backward(self._h, n, *ptrs, *self._ws(workspace, n, dev), _stream_of(dev, stream)))
         return dx, dw, db
 
     def double_backward(self, x, weight, grad_out, h_x=None, h_weight=None, h_bias=None,
@@ -557,20 +577,18 @@ class LayerNorm:
         """The gradients (d grad_out, dx, dweight) of S = <h_x, grad_x> +
         <h_weight, grad_weight> + <h_bias, grad_bias> over the backward; None
         cotangents are zero."""
-        import torch
         n, dev = x.shape[0], x.device
         if grads is None:
-            f = lambda *shape: torch.empty(shape, dtype=torch.float32, device=dev)
-            grads = (f(n, self.d) if "g" in want else None, f(n, self.d) if "x" in want else None,
-                     f(self.n_weight) if "weight" in want else None)
+            grads = (self._like(x, n) if "g" in want else None, self._like(x, n) if "x" in want else None,
+                     self._new(x, self.n_weight) if "weight" in want else None)
         gg, gx, gw = grads
         ptrs = _args(dev, (x, "x", n * self.d, "f32"), (weight, "weight", self.n_weight, "f32"),
                      (grad_out, "grad_out", n * self.d, "f32"), (h_x, "h_x", n * self.d, "f32"),
                      (h_weight, "h_weight", self.n_weight, "f32"), (h_bias, "h_bias", self.n_bias, "f32"),
                      (gg, "grad_grad_out", n * self.d, "f32"), (gx, "grad_x", n * self.d, "f32"),
                      (gw, "grad_weight", self.n_weight, "f32"))
-        _on_current(dev, stream)
-        _check(_lib.cgtp_norm_double_backward(self._h, n, *ptrs, *self._ws(workspace, n, dev), _stream(stream)))
+        _check(_lib.cgtp_norm_double_backward(self._h, n, *ptrs, *self._ws(workspace, n, dev),
+                                              _stream_of(dev, stream)))
         return gg, gx, gw
 
 
@@ -605,12 +623,11 @@ class Router:
     def _gates(self, t, name, n, dev):
         """Pointer and row stride of a [n_experts, n] tensor of unit column
         stride (rows may be padded)."""
-        import torch
         if t is None:
             return None, max(n, 4)
-        if t.dtype != torch.float32:
+        if t.dtype is not _types()["f32"]:
             raise TypeError(f"{name}: expected torch.float32, got {t.dtype}")
-        if tuple(t.shape) != (self.n_experts, n):
+        if t.shape != (self.n_experts, n):
             raise ValueError(f"{name}: expected shape {(self.n_experts, n)}, got {tuple(t.shape)}")
         if not t.is_cuda or (n > 1 and t.stride(1) != 1):
             raise ValueError(f"{name}: expected a CUDA tensor with contiguous rows")
@@ -619,42 +636,39 @@ class Router:
         ld = t.stride(0) if self.n_experts > 1 and n > 0 else -(-n // 4) * 4
         if ld < n:
             raise ValueError(f"{name}: rows overlap (stride {ld}, {n} columns)")
-        return ctypes.c_void_p(t.data_ptr()), ld
+        return t.data_ptr(), ld
 
     def forward(self, logits, bias=None, want=("ids", "weights", "gates", "counts"), outs=None, stream=None):
         """(ids [n, k] int32, weights [n, k], gates [n_experts, n], counts
         [n_experts] int32) of logits [n, n_experts].  The rows of gates are
         16-byte aligned (their stride is n rounded up to 4)."""
-        import torch
         n, dev = logits.shape[0], logits.device
         if outs is None:
-            e = lambda dtype, *shape: torch.empty(shape, dtype=dtype, device=dev)
-            ld = -(-n // 4) * 4
-            outs = (e(torch.int32, n, self.k) if "ids" in want else None,
-                    e(torch.float32, n, self.k) if "weights" in want else None,
-                    e(torch.float32, self.n_experts, ld)[:, :n] if "gates" in want else None,
-                    e(torch.int32, self.n_experts) if "counts" in want else None)
+            f32, i32 = _types()["f32"], _types()["i32"]
+            e = lambda dtype, *shape: logits.new_empty(shape, dtype=dtype)
+            gates = e(f32, self.n_experts, -(-n // 4) * 4) if "gates" in want else None
+            if gates is not None and n % 4:
+                gates = gates[:, :n]
+            outs = (e(i32, n, self.k) if "ids" in want else None, e(f32, n, self.k) if "weights" in want else None,
+                    gates, e(i32, self.n_experts) if "counts" in want else None)
         ids, weights, gates, counts = outs
         pl, pb, pi, pw, pc = _args(dev, (logits, "logits", n * self.n_experts, "f32"),
                                    (bias, "bias", self.n_experts, "f32"), (ids, "ids", n * self.k, "i32"),
                                    (weights, "weights", n * self.k, "f32"),
                                    (counts, "counts", self.n_experts, "i32"))
         pg, ld = self._gates(gates, "gates", n, dev)
-        _on_current(dev, stream)
-        _check(_lib.cgtp_router_forward(self._h, n, pl, pb, pi, pw, pg, ld, pc, _stream(stream)))
+        _check(_lib.cgtp_router_forward(self._h, n, pl, pb, pi, pw, pg, ld, pc, _stream_of(dev, stream)))
         return ids, weights, gates, counts
 
     def backward(self, logits, ids, grad_weights=None, grad_gates=None, grad_logits=None, stream=None):
         """grad_logits [n, n_experts] for grad_weights [n, k] and / or
         grad_gates [n_experts, n] (rows may be padded)."""
-        import torch
         n, dev = logits.shape[0], logits.device
         if grad_logits is None:
-            grad_logits = torch.empty((n, self.n_experts), dtype=torch.float32, device=dev)
+            grad_logits = logits.new_empty((n, self.n_experts), dtype=_types()["f32"])
         pl, pi, pw, po = _args(dev, (logits, "logits", n * self.n_experts, "f32"), (ids, "ids", n * self.k, "i32"),
                                (grad_weights, "grad_weights", n * self.k, "f32"),
                                (grad_logits, "grad_logits", n * self.n_experts, "f32"))
         pg, ld = self._gates(grad_gates, "grad_gates", n, dev)
-        _on_current(dev, stream)
-        _check(_lib.cgtp_router_backward(self._h, n, pl, pi, pw, pg, ld, po, _stream(stream)))
+        _check(_lib.cgtp_router_backward(self._h, n, pl, pi, pw, pg, ld, po, _stream_of(dev, stream)))
         return grad_logits

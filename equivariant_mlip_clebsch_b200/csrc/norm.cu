@@ -22,6 +22,13 @@
 // each CTA leaves one partial sum a channel, and a second launch adds these
 // (no atomics; the order is fixed by n).  Blocks wider than 16,384 values take
 // kernels that read a unit several times.
+//
+// Alignment.  Values move 16 bytes at a time.  Where a block's rows start
+// anywhere (D, its offset or its length no multiple of 4), the rows of a CTA are
+// P = 4 / gcd(D, 4) apart, so that all of them start at the same o = 0..3 floats
+// behind a 16-byte border: value i of the unit is then value i + o of whole
+// float4s, the same thread's in every row, and only the first and the last
+// float4 are moved value by value.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -62,8 +69,9 @@ struct NormArgs {
 struct NormSeg {
   int off, len, d, ch, sc;
   unsigned magic;  // i / d = umulhi(i, magic); 0 for d = 1
-  int tlog, vec;   // log2 of the group's threads; 16-byte columns
-  int cta0, ncta;  // its CTAs
+  int tlog, vec;   // log2 of the group's threads; every row of it whole float4s
+  int period;      // rows of a CTA are so many apart (1, 2 or 4)
+  int cta0, ncta;  // its CTAs, a multiple of period: CTA c has the rows c mod period
   int fin0;        // its first CTA in the closing launch
   int64_t part;    // its partial sums: [ncta][mul] of the weight, then of the bias
 };
@@ -81,6 +89,18 @@ __device__ __forceinline__ void grid_launch_dependents() {
 }
 
 __device__ __forceinline__ int channel_of(int i, unsigned magic) { return magic ? (int)__umulhi(i, magic) : i; }
+
+// Barrier of group g of `width` threads (64 at least).  Immediate numbers: a
+// number in a register would reserve all sixteen barriers for every CTA.
+__device__ __forceinline__ void group_barrier(int g, int width) {
+  switch (g) {
+#define CGTP_GROUP(i) \
+  case i: asm volatile("bar.sync %0, %1;" ::"n"(1 + i), "r"(width) : "memory"); break;
+    CGTP_GROUP(0) CGTP_GROUP(1) CGTP_GROUP(2) CGTP_GROUP(3)
+    CGTP_GROUP(4) CGTP_GROUP(5) CGTP_GROUP(6) CGTP_GROUP(7)
+#undef CGTP_GROUP
+  }
+}
 
 // Sums of K values over a group of 2^tlog threads, the same bits in each of
 // them.  Above a warp: the warps' sums through red (two buffers in turn, so
@@ -102,58 +122,62 @@ __device__ __forceinline__ void group_sum(float (&v)[K], int tlog, float* red, i
 #pragma unroll
     for (int k = 0; k < K; ++k) buf[warp * 8 + k] = v[k];
   }
-  asm volatile("bar.sync %0, %1;" ::"r"(1 + w0 / nw), "r"(width) : "memory");
+  group_barrier(w0 / nw, width);
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = buf[w0 * 8 + k];
-  for (int q = 1; q < nw; ++q) {
+  for (int k = 0; k < K; ++k) v[k] = 0.f;
+  for (int q = 0; q < nw; ++q) {
+    float t[8];
+    const float4* b = reinterpret_cast<const float4*>(buf + (w0 + q) * 8);
+    *reinterpret_cast<float4*>(t) = b[0];
+    if (K > 4) *reinterpret_cast<float4*>(t + 4) = b[1];
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += buf[(w0 + q) * 8 + k];
+    for (int k = 0; k < K; ++k) v[k] += t[k];
   }
 }
 
-// The 4 V values of this thread of one unit: with VEC, float4 v of the thread
-// is float4 v * width + lane of the unit, else value e is value e * width +
-// lane.  m of them exist; the others read as 0.
-template <int V, bool VEC>
-__device__ __forceinline__ void load_unit(const float* p, int width, int lane, int m, float (&v)[4 * V]) {
-  if (VEC) {
+// The 4 V values of this thread of one unit: value j of its slot q is value
+// (q width + lane) 4 + j of the unit's float4s, which start o values before the
+// unit.  It has the slots q < slots; of those in the mask `part` (SHIFT only) just the
+// values in `valid` (bit 4 q + j) belong to the unit: these are moved one by one
+// and the others read as 0.  Slots from `slots` on are not touched.
+template <int V, bool SHIFT>
+__device__ __forceinline__ void load_unit(const float* p, int width, int lane, int slots, unsigned part, unsigned valid,
+                                          float (&v)[4 * V]) {
 #pragma unroll
-    for (int q = 0; q < V; ++q) {
-      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (4 * q < m) t = __ldg(reinterpret_cast<const float4*>(p) + q * width + lane);
-      v[4 * q] = t.x;
-      v[4 * q + 1] = t.y;
-      v[4 * q + 2] = t.z;
-      v[4 * q + 3] = t.w;
+  for (int q = 0; q < V; ++q)
+    if (q < slots) {
+      const float* src = p + 4 * (q * width + lane);
+      if (!SHIFT || !(part >> q & 1)) {
+        const float4 t = __ldg(reinterpret_cast<const float4*>(src));
+        v[4 * q] = t.x;
+        v[4 * q + 1] = t.y;
+        v[4 * q + 2] = t.z;
+        v[4 * q + 3] = t.w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[4 * q + j] = valid >> (4 * q + j) & 1 ? __ldg(src + j) : 0.f;
+      }
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4 * V; ++e) v[e] = e < m ? __ldg(p + e * width + lane) : 0.f;
-  }
 }
 
-template <int V, bool VEC>
 __device__ __forceinline__ void load_slot(const float* s, int width, int lane, int q, float (&v)[4]) {
-  if (VEC) {
-    const float4 t = reinterpret_cast<const float4*>(s)[q * width + lane];
-    v[0] = t.x;
-    v[1] = t.y;
-    v[2] = t.z;
-    v[3] = t.w;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = s[(4 * q + j) * width + lane];
-  }
+  const float4 t = reinterpret_cast<const float4*>(s)[q * width + lane];
+  v[0] = t.x;
+  v[1] = t.y;
+  v[2] = t.z;
+  v[3] = t.w;
 }
 
-template <bool VEC>
-__device__ __forceinline__ void store_slot(float* p, int width, int lane, int q, int m, const float (&v)[4]) {
-  if (VEC) {
-    if (4 * q < m) reinterpret_cast<float4*>(p)[q * width + lane] = make_float4(v[0], v[1], v[2], v[3]);
+template <bool SHIFT>
+__device__ __forceinline__ void store_slot(float* p, int width, int lane, int q, unsigned part, unsigned valid,
+                                           const float (&v)[4]) {
+  float* dst = p + 4 * (q * width + lane);
+  if (!SHIFT || !(part >> q & 1)) {
+    *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (4 * q + j < m) p[(4 * q + j) * width + lane] = v[j];
+      if (valid >> (4 * q + j) & 1) dst[j] = v[j];
   }
 }
 
@@ -168,181 +192,162 @@ __device__ __forceinline__ void add_slot(float4* acc, const float (&v)[4]) {
 
 // The rows of one CTA.  Shared: w (and, by the operator, bias / h_w, h_b)
 // expanded to columns; acc, acc2: the sums of the weight's and the bias's
-// gradient, slot (q, thread).
-template <int OP, int T, int V, bool VEC>
-__device__ __forceinline__ void norm_rows(const NormSeg& s, int D, float eps, int64_t n, const NormArgs& a, bool dw,
+// gradient, slot (q, thread).  CENTRED: a 0e block.
+template <int OP, int T, int V, bool SHIFT, bool CENTRED>
+__device__ __forceinline__ void norm_rows(const NormSeg& s, int o, int D, float eps, int64_t n, const NormArgs& a, bool dw,
                                           bool db, const float* sw, const float* s2, const float* s3, float4* acc,
                                           float4* acc2, float* red) {
   const int width = 1 << s.tlog, lane = threadIdx.x & (width - 1), groups = T >> s.tlog;
   const int cta = blockIdx.x - s.cta0;
-  const int m = VEC ? 4 * max(0, ((s.len >> 2) - lane + width - 1) >> s.tlog)
-                    : max(0, (s.len - lane + width - 1) >> s.tlog);
-  const int64_t step = (int64_t)s.ncta * groups;
+  const int count = SHIFT ? (o + s.len + 3) >> 2 : s.len >> 2;  // float4s of a unit
+  const int have = max(0, (count - lane + width - 1) >> s.tlog);
+  unsigned part = 0, valid = 0xffffffffu;
+  if (SHIFT) {
+    valid = 0;
+#pragma unroll
+    for (int e = 0; e < 4 * V; ++e) {
+      const int i = ((e >> 2) * width + lane) * 4 + (e & 3) - o;
+      valid |= (unsigned)(i >= 0 && i < s.len) << e;
+    }
+#pragma unroll
+    for (int q = 0; q < V; ++q) part |= (unsigned)((valid >> (4 * q) & 15) != 15) << q;
+  }
+  const int period = SHIFT ? s.period : 1, cls = SHIFT ? cta % period : 0;
+  const int64_t step = (int64_t)(SHIFT ? s.ncta / period : s.ncta) * groups;
+  const int64_t rows = SHIFT ? (n - cls + period - 1) / period : n;  // of this CTA's class
   const float inv = 1.f / (float)s.len;
-  const bool centred = s.sc >= 0;
   int turn = 0;
-  for (int64_t r0 = (int64_t)cta * groups; r0 < n; r0 += step) {  // the same trips for every thread of the CTA
-    const int64_t row = r0 + (threadIdx.x >> s.tlog);
-    const int mr = row < n ? m : 0;
-    const int64_t at = row * D + s.off;
-    float x[4 * V];
-    load_unit<V, VEC>(a.x + at, width, lane, mr, x);
-    float mean = 0.f;
-    if (OP == kForward) {
-      if (centred) {
-        float t[1] = {0.f};
+  for (int64_t r0 = (int64_t)(SHIFT ? cta / period : cta) * groups; r0 < rows;
+       r0 += step) {  // the same trips for every thread of the CTA
+    const int64_t mine = r0 + (threadIdx.x >> s.tlog);
+    const int slots = mine < rows ? have : 0;
+    const int64_t at = (SHIFT ? cls + mine * period : mine) * D + s.off - o;
+    float x[4 * V], g[OP == kForward ? 1 : 4 * V], h[OP == kDouble ? 4 * V : 1];
+    load_unit<V, SHIFT>(a.x + at, width, lane, slots, part, valid, x);
+    if constexpr (OP != kForward) load_unit<V, SHIFT>(a.g + at, width, lane, slots, part, valid, g);
+    if constexpr (OP == kDouble) {
+      if (a.hx) {
+        load_unit<V, SHIFT>(a.hx + at, width, lane, slots, part, valid, h);
+      } else {
 #pragma unroll
-        for (int e = 0; e < 4 * V; ++e) t[0] += x[e];
-        group_sum(t, s.tlog, red, turn);
-        mean = t[0] * inv;
+        for (int e = 0; e < 4 * V; ++e) h[e] = 0.f;
       }
-      float t[1] = {0.f};
-#pragma unroll
-      for (int e = 0; e < 4 * V; ++e) {
-        x[e] = e < mr ? x[e] - mean : 0.f;
-        t[0] = fmaf(x[e], x[e], t[0]);
-      }
-      group_sum(t, s.tlog, red, turn);
-      const float r = 1.f / sqrtf(fmaf(t[0], inv, eps));
+    }
+    float mean = 0.f, ma = 0.f, mh = 0.f, mk = 0.f;
+    if (CENTRED) {  // means of x, a = w g, h, k = h_w g
+      constexpr int K = OP == kForward ? 1 : OP == kBackward ? 2 : 4;
+      float t[K] = {};
 #pragma unroll
       for (int q = 0; q < V; ++q)
-        if (4 * q < mr) {
-          float w[4], y[4];
-          load_slot<V, VEC>(sw, width, lane, q, w);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) y[j] = x[4 * q + j] * r * w[j];
-          if (centred) {
-            load_slot<V, VEC>(s2, width, lane, q, w);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] += w[j];
-          }
-          store_slot<VEC>(a.out + at, width, lane, q, mr, y);
-        }
-    } else if (OP == kBackward) {
-      float g[4 * V];
-      load_unit<V, VEC>(a.g + at, width, lane, mr, g);
-      float ma = 0.f;
-      if (centred) {
-        float t[2] = {0.f, 0.f};
-#pragma unroll
-        for (int q = 0; q < V; ++q)
-          if (4 * q < mr) {
-            float w[4];
-            load_slot<V, VEC>(sw, width, lane, q, w);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              t[0] += x[4 * q + j];
-              t[1] = fmaf(g[4 * q + j], w[j], t[1]);
-            }
-          }
-        group_sum(t, s.tlog, red, turn);
-        mean = t[0] * inv;
-        ma = t[1] * inv;
-      }
-      float t[2] = {0.f, 0.f};
-#pragma unroll
-      for (int q = 0; q < V; ++q)
-        if (4 * q < mr) {
-          float w[4];
-          load_slot<V, VEC>(sw, width, lane, q, w);
+        if (q < slots) {
+          float w[4], k[4];
+          if (OP != kForward) load_slot(sw, width, lane, q, w);
+          if (OP == kDouble) load_slot(s2, width, lane, q, k);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int e = 4 * q + j;
-            x[e] = e < mr ? x[e] - mean : 0.f;
-            t[0] = fmaf(x[e], x[e], t[0]);
-            t[1] = fmaf(g[e] * w[j], x[e], t[1]);
-          }
-        }
-      group_sum(t, s.tlog, red, turn);
-      const float r = 1.f / sqrtf(fmaf(t[0], inv, eps));
-      const float al = t[1] * inv * r;
-#pragma unroll
-      for (int q = 0; q < V; ++q)
-        if (4 * q < mr) {
-          float w[4], y[4], p[4], gq[4];
-          load_slot<V, VEC>(sw, width, lane, q, w);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int e = 4 * q + j;
-            const float xh = x[e] * r;
-            gq[j] = g[e];
-            p[j] = g[e] * xh;
-            y[j] = r * (fmaf(g[e], w[j], -ma) - xh * al);
-          }
-          if (a.out) store_slot<VEC>(a.out + at, width, lane, q, mr, y);
-          if (dw) add_slot(acc + q * T + threadIdx.x, p);
-          if (db) add_slot(acc2 + q * T + threadIdx.x, gq);
-        }
-    } else {
-      float g[4 * V], h[4 * V];
-      load_unit<V, VEC>(a.g + at, width, lane, mr, g);
-      load_unit<V, VEC>(a.hx + at, width, lane, a.hx ? mr : 0, h);
-      float ma = 0.f, mk = 0.f;
-      if (centred) {
-        float t[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int q = 0; q < V; ++q)
-          if (4 * q < mr) {
-            float w[4], k[4];
-            load_slot<V, VEC>(sw, width, lane, q, w);
-            load_slot<V, VEC>(s2, width, lane, q, k);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int e = 4 * q + j;
-              t[0] += x[e];
-              t[1] = fmaf(g[e], w[j], t[1]);
+            t[0] += x[e];
+            if constexpr (OP != kForward) t[1] = fmaf(g[e], w[j], t[1]);
+            if constexpr (OP == kDouble) {
               t[2] += h[e];
               t[3] = fmaf(g[e], k[j], t[3]);
             }
           }
-        group_sum(t, s.tlog, red, turn);
-        mean = t[0] * inv;
-        ma = t[1] * inv;
-        const float mh = t[2] * inv;
+        }
+      group_sum(t, s.tlog, red, turn);
+      mean = t[0] * inv;
+      if constexpr (OP != kForward) ma = t[1] * inv;
+      if constexpr (OP == kDouble) {
+        mh = t[2] * inv;
         mk = t[3] * inv;
-#pragma unroll
-        for (int e = 0; e < 4 * V; ++e) h[e] = e < mr ? h[e] - mh : 0.f;
       }
-      float t[5] = {0.f, 0.f, 0.f, 0.f, 0.f};
+    }
+    // sums of xc^2; a xc; h xc, k xc, P h a
+    constexpr int K = OP == kForward ? 1 : OP == kBackward ? 2 : 5;
+    float t[K] = {};
 #pragma unroll
-      for (int q = 0; q < V; ++q)
-        if (4 * q < mr) {
-          float w[4], k[4];
-          load_slot<V, VEC>(sw, width, lane, q, w);
-          load_slot<V, VEC>(s2, width, lane, q, k);
+    for (int q = 0; q < V; ++q)
+      if (q < slots) {
+        float w[4], k[4];
+        if (OP != kForward) load_slot(sw, width, lane, q, w);
+        if (OP == kDouble) load_slot(s2, width, lane, q, k);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int e = 4 * q + j;
-            x[e] = e < mr ? x[e] - mean : 0.f;
+        for (int j = 0; j < 4; ++j) {
+          const int e = 4 * q + j;
+          if (CENTRED) x[e] = !SHIFT || (valid >> e & 1) ? x[e] - mean : 0.f;
+          t[0] = fmaf(x[e], x[e], t[0]);
+          if constexpr (OP == kBackward) t[1] = fmaf(g[e] * w[j], x[e], t[1]);
+          if constexpr (OP == kDouble) {
+            if (CENTRED) h[e] = !SHIFT || (valid >> e & 1) ? h[e] - mh : 0.f;
             const float aa = g[e] * w[j];
-            t[0] = fmaf(x[e], x[e], t[0]);
             t[1] = fmaf(aa, x[e], t[1]);
             t[2] = fmaf(h[e], x[e], t[2]);
             t[3] = fmaf(g[e] * k[j], x[e], t[3]);
             t[4] = fmaf(h[e], aa, t[4]);
           }
         }
-      group_sum(t, s.tlog, red, turn);
-      const float r = 1.f / sqrtf(fmaf(t[0], inv, eps));
-      const float al = t[1] * inv * r, be = t[2] * inv * r, de = t[3] * inv * r, ga = t[4] * inv;
-      const float cx = 3.f * al * be - ga;
+      }
+    group_sum(t, s.tlog, red, turn);
+    const float r = rsqrtf(fmaf(t[0], inv, eps));
+    if constexpr (OP == kForward) {
 #pragma unroll
       for (int q = 0; q < V; ++q)
-        if (4 * q < mr) {
-          float w[4], k[4], b[4] = {0.f, 0.f, 0.f, 0.f}, y[4], z[4], p[4];
-          load_slot<V, VEC>(sw, width, lane, q, w);
-          load_slot<V, VEC>(s2, width, lane, q, k);
-          if (centred) load_slot<V, VEC>(s3, width, lane, q, b);
+        if (q < slots) {
+          float w[4], b[4], y[4];
+          load_slot(sw, width, lane, q, w);
+          if (CENTRED) load_slot(s2, width, lane, q, b);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float xh = x[4 * q + j] * r;
+            y[j] = CENTRED ? fmaf(xh, w[j], b[j]) : xh * w[j];
+          }
+          store_slot<SHIFT>(a.out + at, width, lane, q, part, valid, y);
+        }
+    } else if constexpr (OP == kBackward) {
+      const float al = -t[1] * inv * r;  // grad_x = r (a - mean(a)) + (r al) xh
+      const float shift = -r * ma, along = r * al;
+#pragma unroll
+      for (int q = 0; q < V; ++q)
+        if (q < slots) {
+          float w[4], y[4], p[4], gq[4];
+          load_slot(sw, width, lane, q, w);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int e = 4 * q + j;
-            const float xh = x[e] * r, jh = r * (h[e] - xh * be);
-            y[j] = fmaf(w[j], jh, fmaf(k[j], xh, b[j]));
-            z[j] = r * (r * (xh * cx - be * fmaf(g[e], w[j], -ma) - al * h[e]) + (fmaf(g[e], k[j], -mk) - xh * de));
+            const float xh = x[e] * r;
+            gq[j] = g[e];
+            p[j] = g[e] * xh;
+            const float ra = CENTRED ? fmaf(g[e] * w[j], r, shift) : g[e] * w[j] * r;
+            y[j] = fmaf(xh, along, ra);
+          }
+          if (a.out) store_slot<SHIFT>(a.out + at, width, lane, q, part, valid, y);
+          if (dw) add_slot(acc + q * T + threadIdx.x, p);
+          if (CENTRED && db) add_slot(acc2 + q * T + threadIdx.x, gq);
+        }
+    } else {
+      const float al = t[1] * inv * r, be = t[2] * inv * r, de = t[3] * inv * r, ga = t[4] * inv;
+      // gx = r^2 (cx xh - be P a - al P h) + r (P k - de xh)
+      const float r2 = r * r, cx = r2 * (3.f * al * be - ga) - r * de, rb = -r2 * be, rl = -r2 * al;
+      const float shift = -(rb * ma + r * mk);
+#pragma unroll
+      for (int q = 0; q < V; ++q)
+        if (q < slots) {
+          float w[4], k[4], b[4], y[4], z[4], p[4];
+          load_slot(sw, width, lane, q, w);
+          load_slot(s2, width, lane, q, k);
+          if (CENTRED) load_slot(s3, width, lane, q, b);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int e = 4 * q + j;
+            const float xh = x[e] * r, jh = r * fmaf(-be, xh, h[e]);
+            y[j] = fmaf(w[j], jh, CENTRED ? fmaf(k[j], xh, b[j]) : k[j] * xh);
+            const float c = fmaf(rb, w[j], r * k[j]);  // of g
+            const float lin = fmaf(rl, h[e], xh * cx);
+            z[j] = fmaf(c, g[e], CENTRED ? lin + shift : lin);
             p[j] = g[e] * jh;
           }
-          if (a.out) store_slot<VEC>(a.out + at, width, lane, q, mr, y);
-          if (a.out2) store_slot<VEC>(a.out2 + at, width, lane, q, mr, z);
+          if (a.out) store_slot<SHIFT>(a.out + at, width, lane, q, part, valid, y);
+          if (a.out2) store_slot<SHIFT>(a.out2 + at, width, lane, q, part, valid, z);
           if (dw) add_slot(acc + q * T + threadIdx.x, p);
         }
     }
@@ -355,12 +360,13 @@ constexpr int kRed = 2 * 32 * 8;
 __host__ __device__ constexpr int expanded_arrays(int op, bool centred) {
   return 1 + (op == kForward && centred) + (op == kDouble) + (op == kDouble && centred);
 }
-__host__ __device__ inline int expanded(int len, int tlog) {
+__host__ __device__ inline int expanded(int len, int tlog, int vec) {
   const int slot = 4 << tlog;  // a group's values of one slot
-  return (len + slot - 1) / slot * slot;
+  return (len + (vec ? 0 : 3) + slot - 1) / slot * slot;
 }
 
-template <int OP, int T, int V, int MIN>
+// SHIFT: some block's rows start or end inside a float4.
+template <int OP, int T, int V, bool SHIFT, int MIN>
 __global__ void __launch_bounds__(T, MIN) norm_kernel(const __grid_constant__ NormPlan p, int64_t n,
                                                       const __grid_constant__ NormArgs a, float* __restrict__ part,
                                                       float* __restrict__ dw, float* __restrict__ db) {
@@ -371,7 +377,9 @@ __global__ void __launch_bounds__(T, MIN) norm_kernel(const __grid_constant__ No
   int q = 0;
   while (q + 1 < p.nseg && (int)blockIdx.x >= p.s[q + 1].cta0) ++q;
   const NormSeg s = p.s[q];
-  const int size = expanded(s.len, s.tlog);
+  const int size = expanded(s.len, s.tlog, s.vec);
+  // floats from a 16-byte border to this CTA's units (every array starts on one)
+  const int o = SHIFT ? (int)(((int64_t)((blockIdx.x - s.cta0) % s.period) * p.D + s.off) & 3) : 0;
   float* sw = smem;
   const bool centred = s.sc >= 0;
   float* s2 = sw + size;  // forward: bias of a centred block; double: h_w
@@ -381,8 +389,8 @@ __global__ void __launch_bounds__(T, MIN) norm_kernel(const __grid_constant__ No
   float4* acc2 = acc + (want_w ? T * V : 0);
   float* red = reinterpret_cast<float*>(acc2 + (want_b ? T * V : 0));
   for (int i = threadIdx.x; i < size; i += T) {
-    const int c = channel_of(i, s.magic);
-    const bool in = i < s.len;
+    const bool in = i >= o && i < o + s.len;
+    const int c = in ? channel_of(i - o, s.magic) : 0;
     sw[i] = !in ? 0.f : a.w ? __ldg(a.w + s.ch + c) : 1.f;
     if (OP == kForward && centred) s2[i] = in && a.bias ? __ldg(a.bias + s.sc + c) : 0.f;
     if (OP == kDouble) s2[i] = in && a.hw ? __ldg(a.hw + s.ch + c) : 0.f;
@@ -393,10 +401,10 @@ __global__ void __launch_bounds__(T, MIN) norm_kernel(const __grid_constant__ No
     for (int i = threadIdx.x; i < (want_w ? T * V : 0) + (want_b ? T * V : 0); i += T) acc[i] = zero;
   }
   __syncthreads();
-  if (s.vec)
-    norm_rows<OP, T, V, true>(s, p.D, p.eps, n, a, want_w, want_b, sw, s2, s3, acc, acc2, red);
+  if (centred)
+    norm_rows<OP, T, V, SHIFT, true>(s, o, p.D, p.eps, n, a, want_w, want_b, sw, s2, s3, acc, acc2, red);
   else
-    norm_rows<OP, T, V, false>(s, p.D, p.eps, n, a, want_w, want_b, sw, s2, s3, acc, acc2, red);
+    norm_rows<OP, T, V, SHIFT, false>(s, o, p.D, p.eps, n, a, want_w, want_b, sw, s2, s3, acc, acc2, red);
   if (OP == kForward || (!want_w && !want_b)) return;
   // this CTA's sums: over its groups and over a channel's components
   __syncthreads();
@@ -404,10 +412,8 @@ __global__ void __launch_bounds__(T, MIN) norm_kernel(const __grid_constant__ No
   for (int c = threadIdx.x; c < mul; c += T) {
     float v = 0.f, b = 0.f;
     for (int k = 0; k < s.d; ++k) {
-      const int i = c * s.d + k;
-      const int e = s.vec ? (i >> 2 >> s.tlog) * 4 + (i & 3) : i >> s.tlog;
-      const int lane = s.vec ? (i >> 2) & (width - 1) : i & (width - 1);
-      const int at = ((e >> 2) * T + lane) * 4 + (e & 3);
+      const int i = c * s.d + k + o;
+      const int at = ((i >> 2 >> s.tlog) * T + ((i >> 2) & (width - 1))) * 4 + (i & 3);
       for (int u = 0; u < groups; ++u) {
         if (want_w) v += reinterpret_cast<float*>(acc)[at + u * width * 4];
         if (want_b) b += reinterpret_cast<float*>(acc2)[at + u * width * 4];
@@ -636,23 +642,38 @@ constexpr int kNarrow = 4096;    // values a group of 256 threads holds, 16 a th
 constexpr int kMiddle = 16384;   // values a group of 512 threads holds, 32 a thread
 constexpr size_t kMaxShared = 227 * 1024;
 
-int widest(const NormTable& t) {
-  int m = 0;
-  for (int q = 0; q < t.nblocks; ++q) m = std::max(m, t.b[q].len);
-  return m;
+bool whole(const NormTable& t, const NormBlock& b) { return t.D % 4 == 0 && b.off % 4 == 0 && b.len % 4 == 0; }
+
+// Does every block fit `most` values, wherever its rows start?
+bool fits(const NormTable& t, int most) {
+  for (int q = 0; q < t.nblocks; ++q)
+    if (t.b[q].len + (whole(t, t.b[q]) ? 0 : 3) > most) return false;
+  return true;
 }
 
-// CTAs of a launch: as many as are resident (the backward operators keep sums
-// per CTA), twice that for the forward.
-int target_ctas(int op, bool narrow) { return kSms * (narrow ? (op == kForward ? 12 : 4) : (op == kForward ? 4 : 1)); }
+bool any_shift(const NormTable& t) {
+  for (int q = 0; q < t.nblocks; ++q)
+    if (!whole(t, t.b[q])) return true;
+  return false;
+}
+
+// Resident CTAs an SM, by registers (the launch bounds below).
+constexpr int resident(int op, bool narrow, bool shift) {
+  return narrow ? (op == kForward ? 4 : op == kBackward ? (shift ? 3 : 4) : 2) : (op == kForward ? (shift ? 1 : 2) : 1);
+}
+
+// CTAs of a launch: for the backward operators, which keep sums per CTA, one
+// wave; the forward takes three, so that blocks of unlike cost even out.
+int target_ctas(int op, bool narrow, bool shift) {
+  return kSms * resident(op, narrow, shift) * (op == kForward ? 3 : 1);
+}
 
 // The division of n rows among the CTAs; *floats: the partial sums' size,
 // *shared: bytes of shared memory.  False where some block does not fit a
 // CTA's registers or shared memory (the kernels for wide blocks run then).
 bool norm_plan(const NormTable& t, int op, int64_t n, NormPlan& p, int64_t* floats, size_t* shared) {
-  const int wide = widest(t);
-  if (wide > kMiddle) return false;
-  const bool narrow = wide <= kNarrow;
+  if (!fits(t, kMiddle)) return false;
+  const bool narrow = fits(t, kNarrow), shift = any_shift(t);
   const int T = narrow ? 256 : 512, V = narrow ? 4 : 8;
   p.D = t.D;
   p.nseg = t.nblocks;
@@ -670,12 +691,13 @@ bool norm_plan(const NormTable& t, int op, int64_t n, NormPlan& p, int64_t* floa
     s.ch = b.ch;
     s.sc = b.sc;
     s.magic = b.d == 1 ? 0u : (unsigned)((uint64_t(1) << 32) / b.d + 1);
-    s.vec = t.D % 4 == 0 && b.off % 4 == 0 && b.len % 4 == 0;
+    s.vec = whole(t, b);
     s.tlog = 0;
-    while ((4 * V << s.tlog) < b.len) ++s.tlog;
-    const int64_t groups = T >> s.tlog, need = (n + groups - 1) / groups;
-    const int64_t share = ((int64_t)target_ctas(op, narrow) * b.len + t.D - 1) / t.D;
-    s.ncta = (int)std::max<int64_t>(1, std::min(need, share));
+    s.period = t.D % 4 == 0 ? 1 : t.D % 2 == 0 ? 2 : 4;
+    while ((4 * V << s.tlog) < b.len + (s.vec ? 0 : 3)) ++s.tlog;
+    const int64_t groups = T >> s.tlog, need = ((n + s.period - 1) / s.period + groups - 1) / groups;
+    const int64_t share = (int64_t)target_ctas(op, narrow, shift) * b.len / t.D / s.period;
+    s.ncta = s.period * (int)std::max<int64_t>(1, std::min(need, share));
     s.cta0 = cta;
     cta += s.ncta;
     s.fin0 = fin;
@@ -684,7 +706,7 @@ bool norm_plan(const NormTable& t, int op, int64_t n, NormPlan& p, int64_t* floa
     s.part = part;
     part += (int64_t)s.ncta * mul * (op == kBackward && b.sc >= 0 ? 2 : 1);
     if (s.ncta > 1) p.direct = 0;
-    size_t floats_here = (size_t)expanded_arrays(op, b.sc >= 0) * expanded(b.len, s.tlog) + kRed;
+    size_t floats_here = (size_t)expanded_arrays(op, b.sc >= 0) * expanded(b.len, s.tlog, s.vec) + kRed;
     if (op != kForward) floats_here += (size_t)4 * T * V * (op == kBackward && b.sc >= 0 ? 2 : 1);
     most = std::max(most, floats_here * sizeof(float));
   }
@@ -726,10 +748,10 @@ cudaError_t launch_dependent(void (*kernel)(KArgs...), unsigned grid, unsigned b
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-template <int OP, int T, int V, int MIN>
+template <int OP, int T, int V, bool SHIFT, int MIN>
 cudaError_t launch_rows(const NormPlan& p, int64_t n, const NormArgs& a, size_t shared, float* dw, float* db,
                         float* part, cudaStream_t s) {
-  auto kernel = norm_kernel<OP, T, V, MIN>;
+  auto kernel = norm_kernel<OP, T, V, SHIFT, MIN>;
   if (shared > 48 * 1024) {
     // always the same value: threads with other sizes do not undo it
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxShared);
@@ -757,10 +779,12 @@ cudaError_t launch_norm(const NormTable& t, int64_t n, const NormArgs& a, float*
     return cudaGetLastError();
   }
   float* part = (float*)workspace;
-  const cudaError_t e =
-      widest(t) <= kNarrow
-          ? launch_rows<OP, 256, 4, OP == kForward ? 4 : OP == kBackward ? 3 : 2>(p, n, a, shared, dw, db, part, s)
-          : launch_rows<OP, 512, 8, OP == kForward ? 2 : 1>(p, n, a, shared, dw, db, part, s);
+  const bool narrow = fits(t, kNarrow), shift = any_shift(t);
+  auto rows = narrow ? (shift ? launch_rows<OP, 256, 4, true, resident(OP, true, true)>
+                              : launch_rows<OP, 256, 4, false, resident(OP, true, false)>)
+                     : (shift ? launch_rows<OP, 512, 8, true, resident(OP, false, true)>
+                              : launch_rows<OP, 512, 8, false, resident(OP, false, false)>);
+  const cudaError_t e = rows(p, n, a, shared, dw, db, part, s);
   if (e != cudaSuccess || (!dw && !db) || p.direct) return e;
   int fin = 0;
   for (int q = 0; q < t.nblocks; ++q)
