@@ -70,6 +70,7 @@ struct NormSeg {
   int off, len, d, ch, sc;
   unsigned magic;  // i / d = umulhi(i, magic); 0 for d = 1
   int tlog, vec;   // log2 of the group's threads; every row of it whole float4s
+  int slots;       // float4s a thread has of a unit, at most
   int period;      // rows of a CTA are so many apart (1, 2 or 4)
   int cta0, ncta;  // its CTAs, a multiple of period: CTA c has the rows c mod period
   int fin0;        // its first CTA in the closing launch
@@ -90,78 +91,72 @@ __device__ __forceinline__ void grid_launch_dependents() {
 
 __device__ __forceinline__ int channel_of(int i, unsigned magic) { return magic ? (int)__umulhi(i, magic) : i; }
 
-// Barrier of group g of `width` threads (64 at least).  Immediate numbers: a
+// Barrier of group g of 2^TLOG threads (64 at least).  Immediate numbers: a
 // number in a register would reserve all sixteen barriers for every CTA.
-__device__ __forceinline__ void group_barrier(int g, int width) {
+template <int TLOG>
+__device__ __forceinline__ void group_barrier(int g) {
   switch (g) {
 #define CGTP_GROUP(i) \
-  case i: asm volatile("bar.sync %0, %1;" ::"n"(1 + i), "r"(width) : "memory"); break;
+  case i: asm volatile("bar.sync %0, %1;" ::"n"(1 + i), "n"(1 << TLOG) : "memory"); break;
     CGTP_GROUP(0) CGTP_GROUP(1) CGTP_GROUP(2) CGTP_GROUP(3)
-    CGTP_GROUP(4) CGTP_GROUP(5) CGTP_GROUP(6) CGTP_GROUP(7)
 #undef CGTP_GROUP
   }
 }
 
-// Sums of K values over a group of 2^tlog threads, the same bits in each of
+// Sums of K values over a group of 2^TLOG threads, the same bits in each of
 // them.  Above a warp: the warps' sums through red (two buffers in turn, so
-// that one barrier a call is enough), added in warp order.
-template <int K>
-__device__ __forceinline__ void group_sum(float (&v)[K], int tlog, float* red, int& turn) {
-  const int width = 1 << tlog;
+// that one barrier a call is enough), added by a butterfly of their own.
+template <int TLOG, int K>
+__device__ __forceinline__ void group_sum(float (&v)[K], float* red, int& turn) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    if (o < width) {
+  for (int o = (TLOG < 5 ? TLOG : 5) - 1; o >= 0; --o)
 #pragma unroll
-      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], 1 << o);
+  if constexpr (TLOG > 5) {
+    constexpr int nw = 1 << (TLOG - 5);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w0 = warp & ~(nw - 1);
+    float* buf = red + turn;
+    turn ^= 32 * 8;
+    float4* mine = reinterpret_cast<float4*>(buf + warp * 8);
+    if (lane == 0) {
+      mine[0] = make_float4(v[0], v[K > 1 ? 1 : 0], v[K > 2 ? 2 : 0], v[K > 3 ? 3 : 0]);
+      if constexpr (K > 4) mine[1].x = v[4];
     }
-  if (tlog <= 5) return;
-  const int warp = threadIdx.x >> 5, nw = width >> 5, w0 = warp & ~(nw - 1);
-  float* buf = red + turn * 32 * 8;
-  turn ^= 1;
-  if ((threadIdx.x & 31) == 0) {
+    group_barrier<TLOG>(warp >> (TLOG - 5));
+    const float4* theirs = reinterpret_cast<const float4*>(buf + (w0 + (lane & (nw - 1))) * 8);
+    const float4 t = theirs[0];
+    v[0] = t.x;
+    if constexpr (K > 1) v[1] = t.y;
+    if constexpr (K > 2) v[2] = t.z;
+    if constexpr (K > 3) v[3] = t.w;
+    if constexpr (K > 4) v[4] = theirs[1].x;
 #pragma unroll
-    for (int k = 0; k < K; ++k) buf[warp * 8 + k] = v[k];
-  }
-  group_barrier(w0 / nw, width);
+    for (int o = TLOG - 6; o >= 0; --o)
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = 0.f;
-  for (int q = 0; q < nw; ++q) {
-    float t[8];
-    const float4* b = reinterpret_cast<const float4*>(buf + (w0 + q) * 8);
-    *reinterpret_cast<float4*>(t) = b[0];
-    if (K > 4) *reinterpret_cast<float4*>(t + 4) = b[1];
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += t[k];
+      for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], 1 << o);
   }
 }
 
-// The 4 V values of this thread of one unit: value j of its slot q is value
-// (q width + lane) 4 + j of the unit's float4s, which start o values before the
-// unit.  It has the slots q < slots; of those in the mask `part` (SHIFT only) just the
-// values in `valid` (bit 4 q + j) belong to the unit: these are moved one by one
-// and the others read as 0.  Slots from `slots` on are not touched.
-template <int V, bool SHIFT>
-__device__ __forceinline__ void load_unit(const float* p, int width, int lane, int slots, unsigned part, unsigned valid,
-                                          float (&v)[4 * V]) {
-#pragma unroll
-  for (int q = 0; q < V; ++q)
-    if (q < slots) {
-      const float* src = p + 4 * (q * width + lane);
-      if (!SHIFT || !(part >> q & 1)) {
-        const float4 t = __ldg(reinterpret_cast<const float4*>(src));
-        v[4 * q] = t.x;
-        v[4 * q + 1] = t.y;
-        v[4 * q + 2] = t.z;
-        v[4 * q + 3] = t.w;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[4 * q + j] = valid >> (4 * q + j) & 1 ? __ldg(src + j) : 0.f;
-      }
-    }
+__device__ __forceinline__ void take4(float (&v)[4], const float4 t) {
+  v[0] = t.x;
+  v[1] = t.y;
+  v[2] = t.z;
+  v[3] = t.w;
 }
 
-__device__ __forceinline__ void load_slot(const float* s, int width, int lane, int q, float (&v)[4]) {
-  const float4 t = reinterpret_cast<const float4*>(s)[q * width + lane];
+// Four values at p: all of them where whole, else those in `some` (the others
+// are 0).
+template <bool SHIFT>
+__device__ __forceinline__ void load4(const float* p, bool whole, unsigned some, float* v) {
+  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (whole) {
+    t = __ldg(reinterpret_cast<const float4*>(p));
+  } else if (SHIFT && some) {
+    if (some & 1) t.x = __ldg(p);
+    if (some & 2) t.y = __ldg(p + 1);
+    if (some & 4) t.z = __ldg(p + 2);
+    if (some & 8) t.w = __ldg(p + 3);
+  }
   v[0] = t.x;
   v[1] = t.y;
   v[2] = t.z;
@@ -169,19 +164,17 @@ __device__ __forceinline__ void load_slot(const float* s, int width, int lane, i
 }
 
 template <bool SHIFT>
-__device__ __forceinline__ void store_slot(float* p, int width, int lane, int q, unsigned part, unsigned valid,
-                                           const float (&v)[4]) {
-  float* dst = p + 4 * (q * width + lane);
-  if (!SHIFT || !(part >> q & 1)) {
-    *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
-  } else {
+__device__ __forceinline__ void store4(float* p, bool whole, unsigned some, const float (&v)[4]) {
+  if (whole) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else if (SHIFT && some) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (valid >> (4 * q + j) & 1) dst[j] = v[j];
+      if (some >> j & 1) p[j] = v[j];
   }
 }
 
-__device__ __forceinline__ void add_slot(float4* acc, const float (&v)[4]) {
+__device__ __forceinline__ void add4(float4* acc, const float (&v)[4]) {
   float4 t = *acc;
   t.x += v[0];
   t.y += v[1];
@@ -193,46 +186,59 @@ __device__ __forceinline__ void add_slot(float4* acc, const float (&v)[4]) {
 // The rows of one CTA.  Shared: w (and, by the operator, bias / h_w, h_b)
 // expanded to columns; acc, acc2: the sums of the weight's and the bias's
 // gradient, slot (q, thread).  CENTRED: a 0e block.
-template <int OP, int T, int V, bool SHIFT, bool CENTRED>
-__device__ __forceinline__ void norm_rows(const NormSeg& s, int o, int D, float eps, int64_t n, const NormArgs& a, bool dw,
-                                          bool db, const float* sw, const float* s2, const float* s3, float4* acc,
-                                          float4* acc2, float* red) {
-  const int width = 1 << s.tlog, lane = threadIdx.x & (width - 1), groups = T >> s.tlog;
-  const int cta = blockIdx.x - s.cta0;
-  const int count = SHIFT ? (o + s.len + 3) >> 2 : s.len >> 2;  // float4s of a unit
-  const int have = max(0, (count - lane + width - 1) >> s.tlog);
-  unsigned part = 0, valid = 0xffffffffu;
+//
+// Value j of a thread's slot q is value (q W + lane) 4 + j of the unit's
+// float4s, which start o values before the unit.  Lanes without a slot hold
+// zeros there and compute along, without branches: zeros add nothing to the
+// sums (centred values are masked), and what they leave in acc is not read.
+//
+// The group's size W = 2^TLOG is a constant, so that a thread's slots are
+// immediate offsets from one address an array: with W a variable the addresses
+// and conditions were four fifths of the instructions (73 a value instead of
+// about 20), and the backward was bound by their issue.
+template <int OP, int T, int V, bool SHIFT, bool CENTRED, int TLOG>
+__device__ __forceinline__ void norm_rows(const NormSeg& s, int o, int D, float eps, int64_t n, const NormArgs& a,
+                                          bool dw, bool db, const float4* sw, const float4* s2, const float4* s3,
+                                          float4* acc, float4* acc2, float* red) {
+  constexpr int W = 1 << TLOG, groups = T >> TLOG;
+  const int lane = threadIdx.x & (W - 1);
+  const int cta = blockIdx.x - s.cta0, period = SHIFT ? s.period : 1, cls = SHIFT ? cta % period : 0;
+  const int len = s.len, slots = s.slots;
+  unsigned valid = 0;  // SHIFT: bit 4 q + j: the value belongs to the unit
   if (SHIFT) {
-    valid = 0;
 #pragma unroll
     for (int e = 0; e < 4 * V; ++e) {
-      const int i = ((e >> 2) * width + lane) * 4 + (e & 3) - o;
-      valid |= (unsigned)(i >= 0 && i < s.len) << e;
+      const int i = ((e >> 2) * W + lane) * 4 + (e & 3) - o;
+      valid |= (unsigned)(i >= 0 && i < len) << e;
     }
-#pragma unroll
-    for (int q = 0; q < V; ++q) part |= (unsigned)((valid >> (4 * q) & 15) != 15) << q;
   }
-  const int period = SHIFT ? s.period : 1, cls = SHIFT ? cta % period : 0;
-  const int64_t step = (int64_t)(SHIFT ? s.ncta / period : s.ncta) * groups;
-  const int64_t rows = SHIFT ? (n - cls + period - 1) / period : n;  // of this CTA's class
-  const float inv = 1.f / (float)s.len;
+  const int last = (len >> 2) - lane;  // not SHIFT: slot q exists where q W < last
+  const int step = (SHIFT ? s.ncta / period : s.ncta) * groups;
+  const int rows = (int)(SHIFT ? (n - cls + period - 1) / period : n);  // of this CTA's class
+  const float inv = 1.f / (float)len;
+  sw += lane;
+  s2 += lane;
+  s3 += lane;
+  acc += threadIdx.x;
+  acc2 += threadIdx.x;
   int turn = 0;
-  for (int64_t r0 = (int64_t)(SHIFT ? cta / period : cta) * groups; r0 < rows;
-       r0 += step) {  // the same trips for every thread of the CTA
-    const int64_t mine = r0 + (threadIdx.x >> s.tlog);
-    const int slots = mine < rows ? have : 0;
-    const int64_t at = (SHIFT ? cls + mine * period : mine) * D + s.off - o;
+  int left = rows - (SHIFT ? cta / period : cta) * groups;  // rows from the CTA's first one on
+  const int group = threadIdx.x >> TLOG;
+  int64_t at = ((int64_t)(rows - left + group) * period + cls) * D + s.off - o + 4 * lane;
+  const int64_t stride = (int64_t)step * period * D;
+  for (; left > 0; left -= step, at += stride) {  // the same trips for every thread of the CTA
+    const bool row = group < left;
     float x[4 * V], g[OP == kForward ? 1 : 4 * V], h[OP == kDouble ? 4 * V : 1];
-    load_unit<V, SHIFT>(a.x + at, width, lane, slots, part, valid, x);
-    if constexpr (OP != kForward) load_unit<V, SHIFT>(a.g + at, width, lane, slots, part, valid, g);
-    if constexpr (OP == kDouble) {
-      if (a.hx) {
-        load_unit<V, SHIFT>(a.hx + at, width, lane, slots, part, valid, h);
-      } else {
 #pragma unroll
-        for (int e = 0; e < 4 * V; ++e) h[e] = 0.f;
+    for (int q = 0; q < V; ++q)
+      if (q < slots) {
+        const unsigned some = SHIFT && row ? valid >> (4 * q) & 15 : 0;
+        const bool whole = SHIFT ? some == 15 : row && q * W < last;
+        load4<SHIFT>(a.x + at + 4 * q * W, whole, some, x + 4 * q);
+        if constexpr (OP != kForward) load4<SHIFT>(a.g + at + 4 * q * W, whole, some, g + 4 * q);
+        if constexpr (OP == kDouble)
+          load4<SHIFT>(a.hx + at + 4 * q * W, a.hx && whole, a.hx ? some : 0, h + 4 * q);
       }
-    }
     float mean = 0.f, ma = 0.f, mh = 0.f, mk = 0.f;
     if (CENTRED) {  // means of x, a = w g, h, k = h_w g
       constexpr int K = OP == kForward ? 1 : OP == kBackward ? 2 : 4;
@@ -241,8 +247,8 @@ __device__ __forceinline__ void norm_rows(const NormSeg& s, int o, int D, float 
       for (int q = 0; q < V; ++q)
         if (q < slots) {
           float w[4], k[4];
-          if (OP != kForward) load_slot(sw, width, lane, q, w);
-          if (OP == kDouble) load_slot(s2, width, lane, q, k);
+          if (OP != kForward) take4(w, sw[q * W]);
+          if (OP == kDouble) take4(k, s2[q * W]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int e = 4 * q + j;
@@ -254,7 +260,7 @@ __device__ __forceinline__ void norm_rows(const NormSeg& s, int o, int D, float 
             }
           }
         }
-      group_sum(t, s.tlog, red, turn);
+      group_sum<TLOG>(t, red, turn);
       mean = t[0] * inv;
       if constexpr (OP != kForward) ma = t[1] * inv;
       if constexpr (OP == kDouble) {
@@ -269,16 +275,17 @@ __device__ __forceinline__ void norm_rows(const NormSeg& s, int o, int D, float 
     for (int q = 0; q < V; ++q)
       if (q < slots) {
         float w[4], k[4];
-        if (OP != kForward) load_slot(sw, width, lane, q, w);
-        if (OP == kDouble) load_slot(s2, width, lane, q, k);
+        if (OP != kForward) take4(w, sw[q * W]);
+        if (OP == kDouble) take4(k, s2[q * W]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int e = 4 * q + j;
-          if (CENTRED) x[e] = !SHIFT || (valid >> e & 1) ? x[e] - mean : 0.f;
+          const bool in = SHIFT ? valid >> e & 1 : q * W < last;
+          if (CENTRED) x[e] = in ? x[e] - mean : 0.f;
           t[0] = fmaf(x[e], x[e], t[0]);
           if constexpr (OP == kBackward) t[1] = fmaf(g[e] * w[j], x[e], t[1]);
           if constexpr (OP == kDouble) {
-            if (CENTRED) h[e] = !SHIFT || (valid >> e & 1) ? h[e] - mh : 0.f;
+            if (CENTRED) h[e] = in ? h[e] - mh : 0.f;
             const float aa = g[e] * w[j];
             t[1] = fmaf(aa, x[e], t[1]);
             t[2] = fmaf(h[e], x[e], t[2]);
@@ -287,70 +294,89 @@ __device__ __forceinline__ void norm_rows(const NormSeg& s, int o, int D, float 
           }
         }
       }
-    group_sum(t, s.tlog, red, turn);
+    group_sum<TLOG>(t, red, turn);
     const float r = rsqrtf(fmaf(t[0], inv, eps));
-    if constexpr (OP == kForward) {
+    float along = 0.f, shift = 0.f, be = 0.f, rb = 0.f, rl = 0.f;
+    if constexpr (OP == kBackward) {  // grad_x = r (a - mean(a)) - (r al) xh
+      along = -r * (t[1] * inv * r);
+      shift = -r * ma;
+    }
+    if constexpr (OP == kDouble) {  // gx = r^2 (cx xh - be P a - al P h) + r (P k - de xh)
+      const float al = t[1] * inv * r, de = t[3] * inv * r, ga = t[4] * inv;
+      be = t[2] * inv * r;
+      along = r * r * (3.f * al * be - ga) - r * de;
+      rb = -r * r * be;
+      rl = -r * r * al;
+      shift = -(rb * ma + r * mk);
+    }
 #pragma unroll
-      for (int q = 0; q < V; ++q)
-        if (q < slots) {
-          float w[4], b[4], y[4];
-          load_slot(sw, width, lane, q, w);
-          if (CENTRED) load_slot(s2, width, lane, q, b);
+    for (int q = 0; q < V; ++q)
+      if (q < slots) {
+        const unsigned some = SHIFT && row ? valid >> (4 * q) & 15 : 0;
+        const bool whole = SHIFT ? some == 15 : row && q * W < last;
+        float w[4], y[4];
+        take4(w, sw[q * W]);
+        if constexpr (OP == kForward) {
+          float b[4];
+          if (CENTRED) take4(b, s2[q * W]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float xh = x[4 * q + j] * r;
             y[j] = CENTRED ? fmaf(xh, w[j], b[j]) : xh * w[j];
           }
-          store_slot<SHIFT>(a.out + at, width, lane, q, part, valid, y);
-        }
-    } else if constexpr (OP == kBackward) {
-      const float al = -t[1] * inv * r;  // grad_x = r (a - mean(a)) + (r al) xh
-      const float shift = -r * ma, along = r * al;
-#pragma unroll
-      for (int q = 0; q < V; ++q)
-        if (q < slots) {
-          float w[4], y[4], p[4], gq[4];
-          load_slot(sw, width, lane, q, w);
+          store4<SHIFT>(a.out + at + 4 * q * W, whole, some, y);
+        } else if constexpr (OP == kBackward) {
+          float p[4], gq[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int e = 4 * q + j;
             const float xh = x[e] * r;
             gq[j] = g[e];
             p[j] = g[e] * xh;
-            const float ra = CENTRED ? fmaf(g[e] * w[j], r, shift) : g[e] * w[j] * r;
-            y[j] = fmaf(xh, along, ra);
+            y[j] = fmaf(xh, along, CENTRED ? fmaf(g[e] * w[j], r, shift) : g[e] * w[j] * r);
           }
-          if (a.out) store_slot<SHIFT>(a.out + at, width, lane, q, part, valid, y);
-          if (dw) add_slot(acc + q * T + threadIdx.x, p);
-          if (CENTRED && db) add_slot(acc2 + q * T + threadIdx.x, gq);
-        }
-    } else {
-      const float al = t[1] * inv * r, be = t[2] * inv * r, de = t[3] * inv * r, ga = t[4] * inv;
-      // gx = r^2 (cx xh - be P a - al P h) + r (P k - de xh)
-      const float r2 = r * r, cx = r2 * (3.f * al * be - ga) - r * de, rb = -r2 * be, rl = -r2 * al;
-      const float shift = -(rb * ma + r * mk);
-#pragma unroll
-      for (int q = 0; q < V; ++q)
-        if (q < slots) {
-          float w[4], k[4], b[4], y[4], z[4], p[4];
-          load_slot(sw, width, lane, q, w);
-          load_slot(s2, width, lane, q, k);
-          if (CENTRED) load_slot(s3, width, lane, q, b);
+          if (a.out) store4<SHIFT>(a.out + at + 4 * q * W, whole, some, y);
+          if (dw) add4(acc + q * T, p);
+          if (CENTRED && db) add4(acc2 + q * T, gq);
+        } else {
+          float k[4], b[4], z[4], p[4];
+          take4(k, s2[q * W]);
+          if (CENTRED) take4(b, s3[q * W]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int e = 4 * q + j;
             const float xh = x[e] * r, jh = r * fmaf(-be, xh, h[e]);
             y[j] = fmaf(w[j], jh, CENTRED ? fmaf(k[j], xh, b[j]) : k[j] * xh);
             const float c = fmaf(rb, w[j], r * k[j]);  // of g
-            const float lin = fmaf(rl, h[e], xh * cx);
+            const float lin = fmaf(rl, h[e], xh * along);
             z[j] = fmaf(c, g[e], CENTRED ? lin + shift : lin);
             p[j] = g[e] * jh;
           }
-          if (a.out) store_slot<SHIFT>(a.out + at, width, lane, q, part, valid, y);
-          if (a.out2) store_slot<SHIFT>(a.out2 + at, width, lane, q, part, valid, z);
-          if (dw) add_slot(acc + q * T + threadIdx.x, p);
+          if (a.out) store4<SHIFT>(a.out + at + 4 * q * W, whole, some, y);
+          if (a.out2) store4<SHIFT>(a.out2 + at + 4 * q * W, whole, some, z);
+          if (dw) add4(acc + q * T, p);
         }
+      }
+  }
+}
+
+// The group sizes that are built: 4, 16, 32, 64, 128 and 256 threads for CTAs
+// of 256 (16 values a thread), 4, 32, 128 and 512 for CTAs of 512 (32 values).
+__host__ __device__ constexpr bool width_built(int tlog, int T) {
+  return T == 256 ? tlog == 2 || (tlog >= 4 && tlog <= 8) : tlog == 2 || tlog == 5 || tlog == 7 || tlog == 9;
+}
+
+template <int OP, int T, int V, bool SHIFT, int TLOG = 2, class... Rest>
+__device__ __forceinline__ void norm_width(const NormSeg& s, Rest... rest) {
+  if (s.tlog == TLOG) {
+    if constexpr (width_built(TLOG, T)) {
+      if (s.sc >= 0)
+        norm_rows<OP, T, V, SHIFT, true, TLOG>(s, rest...);
+      else
+        norm_rows<OP, T, V, SHIFT, false, TLOG>(s, rest...);
     }
+  } else if constexpr ((2 << TLOG) <= T) {
+    norm_width<OP, T, V, SHIFT, TLOG + 1>(s, rest...);
   }
 }
 
@@ -401,10 +427,8 @@ __global__ void __launch_bounds__(T, MIN) norm_kernel(const __grid_constant__ No
     for (int i = threadIdx.x; i < (want_w ? T * V : 0) + (want_b ? T * V : 0); i += T) acc[i] = zero;
   }
   __syncthreads();
-  if (centred)
-    norm_rows<OP, T, V, SHIFT, true>(s, o, p.D, p.eps, n, a, want_w, want_b, sw, s2, s3, acc, acc2, red);
-  else
-    norm_rows<OP, T, V, SHIFT, false>(s, o, p.D, p.eps, n, a, want_w, want_b, sw, s2, s3, acc, acc2, red);
+  const float4 *sw4 = smem4, *s24 = sw4 + size / 4, *s34 = s24 + size / 4;
+  norm_width<OP, T, V, SHIFT>(s, o, p.D, p.eps, n, a, want_w, want_b, sw4, s24, s34, acc, acc2, red);
   if (OP == kForward || (!want_w && !want_b)) return;
   // this CTA's sums: over its groups and over a channel's components
   __syncthreads();
@@ -467,7 +491,7 @@ constexpr int kWide = 256;
 
 __device__ __forceinline__ float cta_sum(float v, float* red, int& turn) {
   float t[1] = {v};
-  group_sum(t, 8, red, turn);
+  group_sum<8>(t, red, turn);
   return t[0];
 }
 
@@ -682,6 +706,16 @@ bool norm_plan(const NormTable& t, int op, int64_t n, NormPlan& p, int64_t* floa
   int cta = 0, fin = 0;
   int64_t part = 0;
   size_t most = 0;
+  // A unit's cost to its group: the threads' values, and as much as eight more a
+  // thread for the sums.
+  auto cost = [](int len, int tlog) { return (double)len + (8 << tlog); };
+  auto threads_log = [&](const NormBlock& b) {
+    int k = 0;
+    while (!width_built(k, T) || (4 * V << k) < b.len + (whole(t, b) ? 0 : 3)) ++k;
+    return k;
+  };
+  double all = 0;
+  for (int q = 0; q < t.nblocks; ++q) all += cost(t.b[q].len, threads_log(t.b[q]));
   for (int q = 0; q < t.nblocks; ++q) {
     const NormBlock& b = t.b[q];
     NormSeg& s = p.s[q];
@@ -692,11 +726,11 @@ bool norm_plan(const NormTable& t, int op, int64_t n, NormPlan& p, int64_t* floa
     s.sc = b.sc;
     s.magic = b.d == 1 ? 0u : (unsigned)((uint64_t(1) << 32) / b.d + 1);
     s.vec = whole(t, b);
-    s.tlog = 0;
+    s.tlog = threads_log(b);
     s.period = t.D % 4 == 0 ? 1 : t.D % 2 == 0 ? 2 : 4;
-    while ((4 * V << s.tlog) < b.len + (s.vec ? 0 : 3)) ++s.tlog;
+    s.slots = (b.len + (s.vec ? 0 : 3) + (4 << s.tlog) - 1) >> (2 + s.tlog);
     const int64_t groups = T >> s.tlog, need = ((n + s.period - 1) / s.period + groups - 1) / groups;
-    const int64_t share = (int64_t)target_ctas(op, narrow, shift) * b.len / t.D / s.period;
+    const int64_t share = (int64_t)(target_ctas(op, narrow, shift) * cost(b.len, s.tlog) / all) / s.period;
     s.ncta = s.period * (int)std::max<int64_t>(1, std::min(need, share));
     s.cta0 = cta;
     cta += s.ncta;
