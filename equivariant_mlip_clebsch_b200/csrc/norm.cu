@@ -174,13 +174,13 @@ __device__ __forceinline__ void store4(float* p, bool whole, unsigned some, cons
   }
 }
 
-__device__ __forceinline__ void add4(float4* acc, const float (&v)[4]) {
-  float4 t = *acc;
-  t.x += v[0];
-  t.y += v[1];
-  t.z += v[2];
-  t.w += v[3];
-  *acc = t;
+__device__ __forceinline__ void add_to(float4& acc, const float4 v) {
+  float4 t = acc;
+  t.x += v.x;
+  t.y += v.y;
+  t.z += v.z;
+  t.w += v.w;
+  acc = t;
 }
 
 // The rows of one CTA.  Shared: w (and, by the operator, bias / h_w, h_b)
@@ -336,8 +336,8 @@ __device__ __forceinline__ void norm_rows(const NormSeg& s, int o, int D, float 
             y[j] = fmaf(xh, along, CENTRED ? fmaf(g[e] * w[j], r, shift) : g[e] * w[j] * r);
           }
           if (a.out) store4<SHIFT>(a.out + at + 4 * q * W, whole, some, y);
-          if (dw) add4(acc + q * T, p);
-          if (CENTRED && db) add4(acc2 + q * T, gq);
+          if (dw) add_to(acc[q * T], make_float4(p[0], p[1], p[2], p[3]));
+          if (CENTRED && db) add_to(acc2[q * T], make_float4(gq[0], gq[1], gq[2], gq[3]));
         } else {
           float k[4], b[4], z[4], p[4];
           take4(k, s2[q * W]);
@@ -354,7 +354,7 @@ __device__ __forceinline__ void norm_rows(const NormSeg& s, int o, int D, float 
           }
           if (a.out) store4<SHIFT>(a.out + at + 4 * q * W, whole, some, y);
           if (a.out2) store4<SHIFT>(a.out2 + at + 4 * q * W, whole, some, z);
-          if (dw) add4(acc + q * T, p);
+          if (dw) add_to(acc[q * T], make_float4(p[0], p[1], p[2], p[3]));
         }
       }
   }
@@ -430,18 +430,24 @@ __global__ void __launch_bounds__(T, MIN) norm_kernel(const __grid_constant__ No
   const float4 *sw4 = smem4, *s24 = sw4 + size / 4, *s34 = s24 + size / 4;
   norm_width<OP, T, V, SHIFT>(s, o, p.D, p.eps, n, a, want_w, want_b, sw4, s24, s34, acc, acc2, red);
   if (OP == kForward || (!want_w && !want_b)) return;
-  // this CTA's sums: over its groups and over a channel's components
+  // this CTA's sums: over its groups, halving them, then over a channel's components
+  const int mul = s.len / s.d, width = 1 << s.tlog, cta = blockIdx.x - s.cta0;
+  for (int h = T / 2; h >= width; h >>= 1) {
+    __syncthreads();
+    if ((int)threadIdx.x < h)
+      for (int k = 0; k < s.slots; ++k) {
+        if (want_w) add_to(acc[k * T + threadIdx.x], acc[k * T + threadIdx.x + h]);
+        if (want_b) add_to(acc2[k * T + threadIdx.x], acc2[k * T + threadIdx.x + h]);
+      }
+  }
   __syncthreads();
-  const int mul = s.len / s.d, width = 1 << s.tlog, groups = T >> s.tlog, cta = blockIdx.x - s.cta0;
   for (int c = threadIdx.x; c < mul; c += T) {
     float v = 0.f, b = 0.f;
     for (int k = 0; k < s.d; ++k) {
       const int i = c * s.d + k + o;
       const int at = ((i >> 2 >> s.tlog) * T + ((i >> 2) & (width - 1))) * 4 + (i & 3);
-      for (int u = 0; u < groups; ++u) {
-        if (want_w) v += reinterpret_cast<float*>(acc)[at + u * width * 4];
-        if (want_b) b += reinterpret_cast<float*>(acc2)[at + u * width * 4];
-      }
+      if (want_w) v += reinterpret_cast<float*>(acc)[at];
+      if (want_b) b += reinterpret_cast<float*>(acc2)[at];
     }
     if (p.direct) {
       if (want_w) dw[s.ch + c] = v;
@@ -453,13 +459,17 @@ __global__ void __launch_bounds__(T, MIN) norm_kernel(const __grid_constant__ No
   }
 }
 
-// The closing sums: a CTA takes 32 channels of one block; eight warps share
-// the CTAs' partial sums, which are then added in warp order.
-__global__ void __launch_bounds__(256) norm_finish_kernel(const __grid_constant__ NormPlan p,
-                                                          const float* __restrict__ part, float* __restrict__ dw,
-                                                          float* __restrict__ db) {
+// The closing sums: a CTA takes 32 channels of one block; its warps share the
+// CTAs' partial sums, eight loads in flight each, which are then added in warp
+// order.
+constexpr int kFinish = 1024;
+
+__global__ void __launch_bounds__(kFinish) norm_finish_kernel(const __grid_constant__ NormPlan p,
+                                                              const float* __restrict__ part, float* __restrict__ dw,
+                                                              float* __restrict__ db) {
   grid_dependency_wait();
   grid_launch_dependents();
+  constexpr int kWarps = kFinish / 32;
   int q = 0;
   while (q + 1 < p.nseg && (int)blockIdx.x >= p.s[q + 1].fin0) ++q;
   const NormSeg s = p.s[q];
@@ -472,17 +482,25 @@ __global__ void __launch_bounds__(256) norm_finish_kernel(const __grid_constant_
   float v = 0.f;
   if (c < mul) {
     const float* src = part + s.part + (bias ? (int64_t)s.ncta * mul : 0) + c;
-#pragma unroll 4
-    for (int k = warp; k < s.ncta; k += 8) v += src[(int64_t)k * mul];
+    for (int k0 = warp; k0 < s.ncta; k0 += 8 * kWarps) {
+      float t[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int k = k0 + j * kWarps;
+        t[j] = k < s.ncta ? src[(int64_t)k * mul] : 0.f;
+      }
+      v += ((t[0] + t[1]) + (t[2] + t[3])) + ((t[4] + t[5]) + (t[6] + t[7]));
+    }
   }
-  __shared__ float sums[8][32];
+  __shared__ float sums[kWarps][33];
   sums[warp][lane] = v;
   __syncthreads();
-  if (warp == 0 && c < mul) {
+  // warp w adds the partial sums of channel w
+  v = sums[lane][warp];
 #pragma unroll
-    for (int k = 1; k < 8; ++k) v += sums[k][lane];
-    out[c] = v;
-  }
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int mine = (bias ? tile - tiles : tile) * 32 + warp;
+  if (lane == 0 && mine < mul) out[mine] = v;
 }
 
 // ---- blocks wider than the registers of a CTA: one CTA a unit, several reads
@@ -665,6 +683,7 @@ constexpr int kSms = 148;
 constexpr int kNarrow = 4096;    // values a group of 256 threads holds, 16 a thread
 constexpr int kMiddle = 16384;   // values a group of 512 threads holds, 32 a thread
 constexpr size_t kMaxShared = 227 * 1024;
+constexpr int64_t kDirectTrips = 4;
 
 bool whole(const NormTable& t, const NormBlock& b) { return t.D % 4 == 0 && b.off % 4 == 0 && b.len % 4 == 0; }
 
@@ -686,15 +705,13 @@ constexpr int resident(int op, bool narrow, bool shift) {
   return narrow ? (op == kForward ? 4 : op == kBackward ? (shift ? 3 : 4) : 2) : (op == kForward ? (shift ? 1 : 2) : 1);
 }
 
-// CTAs of a launch: for the backward operators, which keep sums per CTA, one
-// wave; the forward takes three, so that blocks of unlike cost even out.
-int target_ctas(int op, bool narrow, bool shift) {
-  return kSms * resident(op, narrow, shift) * (op == kForward ? 3 : 1);
-}
-
 // The division of n rows among the CTAs; *floats: the partial sums' size,
 // *shared: bytes of shared memory.  False where some block does not fit a
 // CTA's registers or shared memory (the kernels for wide blocks run then).
+//
+// One wave of CTAs.  A CTA's trip over one row a group costs about its threads' slots
+// and two slots' time more for the sums, so the blocks' CTAs are chosen for the
+// smallest bound on trips x cost that one wave meets.
 bool norm_plan(const NormTable& t, int op, int64_t n, NormPlan& p, int64_t* floats, size_t* shared) {
   if (!fits(t, kMiddle)) return false;
   const bool narrow = fits(t, kNarrow), shift = any_shift(t);
@@ -702,20 +719,9 @@ bool norm_plan(const NormTable& t, int op, int64_t n, NormPlan& p, int64_t* floa
   p.D = t.D;
   p.nseg = t.nblocks;
   p.eps = t.eps;
-  p.direct = 1;
-  int cta = 0, fin = 0;
-  int64_t part = 0;
-  size_t most = 0;
-  // A unit's cost to its group: the threads' values, and as much as eight more a
-  // thread for the sums.
-  auto cost = [](int len, int tlog) { return (double)len + (8 << tlog); };
-  auto threads_log = [&](const NormBlock& b) {
-    int k = 0;
-    while (!width_built(k, T) || (4 * V << k) < b.len + (whole(t, b) ? 0 : 3)) ++k;
-    return k;
-  };
-  double all = 0;
-  for (int q = 0; q < t.nblocks; ++q) all += cost(t.b[q].len, threads_log(t.b[q]));
+  int64_t trips[kMaxBlocks];  // of a class of rows, by one CTA
+  int cost[kMaxBlocks];
+  int64_t work = 0, longest = 1;
   for (int q = 0; q < t.nblocks; ++q) {
     const NormBlock& b = t.b[q];
     NormSeg& s = p.s[q];
@@ -726,23 +732,45 @@ bool norm_plan(const NormTable& t, int op, int64_t n, NormPlan& p, int64_t* floa
     s.sc = b.sc;
     s.magic = b.d == 1 ? 0u : (unsigned)((uint64_t(1) << 32) / b.d + 1);
     s.vec = whole(t, b);
-    s.tlog = threads_log(b);
     s.period = t.D % 4 == 0 ? 1 : t.D % 2 == 0 ? 2 : 4;
-    s.slots = (b.len + (s.vec ? 0 : 3) + (4 << s.tlog) - 1) >> (2 + s.tlog);
-    const int64_t groups = T >> s.tlog, need = ((n + s.period - 1) / s.period + groups - 1) / groups;
-    const int64_t share = (int64_t)(target_ctas(op, narrow, shift) * cost(b.len, s.tlog) / all) / s.period;
-    s.ncta = s.period * (int)std::max<int64_t>(1, std::min(need, share));
+    const int values = b.len + (s.vec ? 0 : 3);
+    s.tlog = 0;
+    while (!width_built(s.tlog, T) || (4 * V << s.tlog) < values) ++s.tlog;
+    s.slots = (values + (4 << s.tlog) - 1) >> (2 + s.tlog);
+    const int64_t groups = T >> s.tlog, rows = (n + s.period - 1) / s.period;
+    trips[q] = (rows + groups - 1) / groups;
+    cost[q] = s.slots + 2;
+    work += trips[q] * s.period * cost[q];
+    longest = std::max(longest, trips[q]);
+  }
+  const int64_t target = kSms * resident(op, narrow, shift);
+  // few rows: one CTA a block writes the gradients itself, without a second launch
+  p.direct = op != kForward && longest <= kDirectTrips && t.D % 4 == 0;
+  for (int64_t bound = std::max<int64_t>(work / target, 1);; bound += bound / 16 + 1) {
+    int64_t total = 0;
+    for (int q = 0; q < t.nblocks; ++q) {
+      const int64_t each = std::max<int64_t>(bound / cost[q], 1);
+      p.s[q].ncta = p.direct ? 1 : (int)(p.s[q].period * std::min<int64_t>((trips[q] + each - 1) / each, target));
+      total += p.s[q].ncta;
+    }
+    if (total <= target || bound >= longest * (V + 2)) break;
+  }
+  int cta = 0, fin = 0;
+  int64_t part = 0;
+  size_t most = 0;
+  for (int q = 0; q < t.nblocks; ++q) {
+    NormSeg& s = p.s[q];
+    const bool two = op == kBackward && s.sc >= 0;
+    const int mul = s.len / s.d;
     s.cta0 = cta;
     cta += s.ncta;
     s.fin0 = fin;
-    const int mul = b.len / b.d, tiles = (mul + 31) / 32;
-    fin += tiles * (op == kBackward && b.sc >= 0 ? 2 : 1);
+    fin += (mul + 31) / 32 * (two ? 2 : 1);
     s.part = part;
-    part += (int64_t)s.ncta * mul * (op == kBackward && b.sc >= 0 ? 2 : 1);
-    if (s.ncta > 1) p.direct = 0;
-    size_t floats_here = (size_t)expanded_arrays(op, b.sc >= 0) * expanded(b.len, s.tlog, s.vec) + kRed;
-    if (op != kForward) floats_here += (size_t)4 * T * V * (op == kBackward && b.sc >= 0 ? 2 : 1);
-    most = std::max(most, floats_here * sizeof(float));
+    part += (int64_t)s.ncta * mul * (two ? 2 : 1);
+    size_t here = (size_t)expanded_arrays(op, s.sc >= 0) * expanded(s.len, s.tlog, s.vec) + kRed;
+    if (op != kForward) here += (size_t)4 * T * V * (two ? 2 : 1);
+    most = std::max(most, here * sizeof(float));
   }
   *floats = part;
   *shared = most;
@@ -823,7 +851,7 @@ cudaError_t launch_norm(const NormTable& t, int64_t n, const NormArgs& a, float*
   int fin = 0;
   for (int q = 0; q < t.nblocks; ++q)
     fin += (t.b[q].len / t.b[q].d + 31) / 32 * (OP == kBackward && t.b[q].sc >= 0 ? 2 : 1);
-  return launch_dependent(norm_finish_kernel, (unsigned)fin, 256, 0, s, p, (const float*)part, dw, db);
+  return launch_dependent(norm_finish_kernel, (unsigned)fin, kFinish, 0, s, p, (const float*)part, dw, db);
 }
 
 }  // namespace
