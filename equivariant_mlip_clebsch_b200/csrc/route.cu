@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include <cfloat>
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <algorithm>
@@ -213,179 +214,274 @@ __global__ void __launch_bounds__(256) route_warp_kernel(RouteSpec p, int64_t n,
 
 // ---- forward, one thread a row (many rows)
 
-constexpr int kRows = 128;         // rows of a CTA's tile
+constexpr int kRows = 128;           // rows of a CTA's tile
 constexpr int kThreadExperts = 128;  // the widest row of this form
 constexpr int kThreadK = 8;
 
 __device__ __forceinline__ float quick_sigmoid(float l) { return __fdividef(1.f, 1.f + __expf(-l)); }
 
+// A key whose order as an integer is the value's, its low bits replaced so that of
+// equal values the lowest index is the largest; mask = 2^bits - 1 >= experts - 1.
+__device__ __forceinline__ int key_of(float v, int e, int mask) {
+  int i = __float_as_int(v);
+  i ^= (i >> 31) & 0x7fffffff;
+  return (i & ~mask) | (mask - e);
+}
+
+// The largest value that a key's order allows.
+__device__ __forceinline__ float key_top(int key, int mask) {
+  int i = key | mask;
+  i ^= (i >> 31) & 0x7fffffff;
+  return __int_as_float(i);
+}
+
 // A row's choice in FP32, by one thread.  Two compared values are off by at
-// most `tol` against one another; where a decision is closer than that the row
-// is marked (unless the two have equal logits and biases) and decided again in
-// 64 bits by the whole warp.
+// most a bound against one another; where a decision is closer than that the row
+// is looked at again (two experts of equal logit and bias are in their right
+// order already) and, if that does not settle it, decided in 64 bits by the
+// whole warp.
 //   sigmoid: 1 / (1 + __expf(-l)): the exponent's rounding and the function's error
 //   give s (1 - s) (|l| 2^-24 + 2^-22) < 8e-8, the division 2 ulp: |ds| < 2e-7
 //   softmax: exp(l - top) off by < 2.7e-7 in the same way; the sum's relative
 //   error, eight partial sums, (n / 8 + 4) 2^-24, is common to all scores <= 1
 //   adding the bias rounds by 2^-24 |v|
-// and a group's score adds two such values.
+// and a group's score adds two such values.  The k + 1 best are found as integer
+// keys (two instructions a place and expert) that hold the index in their
+// low bits; the keys' order is put right from the values themselves.
+//
+// Two threads share a row, each with one half of every group: the second also
+// clears the row's gates while the first chooses the groups.  The tile lies
+// by experts, [expert][row], so that a thread's experts are constant offsets from
+// one address.
 template <int K, bool SIGMOID, bool BY_LOGIT>
-__global__ void __launch_bounds__(kRows) route_thread_kernel(RouteSpec p, int64_t n, const float* __restrict__ logits,
-                                                             const float* __restrict__ bias,
-                                                             int32_t* __restrict__ ids, float* __restrict__ weights,
-                                                             float* __restrict__ gates, int64_t ld,
-                                                             int32_t* __restrict__ counts, unsigned magic) {
+__global__ void __launch_bounds__(2 * kRows) route_thread_kernel(
+    RouteSpec p, int64_t n, const float* __restrict__ logits, const float* __restrict__ bias,
+    int32_t* __restrict__ ids, float* __restrict__ weights, float* __restrict__ gates, int64_t ld,
+    int32_t* __restrict__ counts, unsigned magic) {
   grid_dependency_wait();
   grid_launch_dependents();
   extern __shared__ float smem[];
-  const int stride = p.n | 1, tid = threadIdx.x, lane = tid & 31;
-  float* tile = smem;                                // [kRows][stride]
-  float* sb = tile + kRows * stride;                 // [n] bias
-  int* hist = reinterpret_cast<int*>(sb + p.n);      // [n]
-  float* gsc = reinterpret_cast<float*>(hist + p.n);  // [groups][kRows]
-  for (int e = tid; e < p.n; e += kRows) {
-    sb[e] = bias ? __ldg(bias + e) : 0.f;
+  constexpr int S = kRows + 1;  // odd: neither filling nor reading meets one bank
+  const int tid = threadIdx.x & (kRows - 1), half = threadIdx.x / kRows, lane = tid & 31, N = p.n;
+  float* tile = smem;                                  // [N][S]
+  float* sb = tile + N * S;                            // [N] bias
+  int* hist = reinterpret_cast<int*>(sb + N);          // [N]
+  unsigned* skept = reinterpret_cast<unsigned*>(hist + N);  // [kRows] groups kept
+  float* swap = reinterpret_cast<float*>(skept + kRows);    // [swap_rows][kRows], what the halves tell one another
+  for (int e = threadIdx.x; e < N; e += 2 * kRows) {
+    const float b = bias ? __ldg(bias + e) : 0.f;
+    sb[e] = b >= -INFINITY ? b : -INFINITY;  // a NaN rules the expert out too
     hist[e] = 0;
   }
-  const float base = SIGMOID ? 4e-7f : 6e-7f + (float)(p.n / 8 + 4) * 6e-8f;
-  const int size = p.n / p.groups;
+  int mask = 1;
+  while (mask < N - 1) mask = 2 * mask + 1;
+  const float base = SIGMOID ? 4e-7f : 6e-7f + (float)(N / 8 + 4) * 6e-8f;
+  const int size = N / p.groups, split = (size + 1) / 2;
+  const int from = half ? split : 0, to = half ? size : split;  // this thread's part of a group
   for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < n; t0 += (int64_t)gridDim.x * kRows) {
     const int rows = (int)min((int64_t)kRows, n - t0);
     __syncthreads();  // the tile of the round before is read
-    const float* src = logits + t0 * p.n;  // kRows p.n values from a 16-byte border
-    for (int i = tid * 4; i < rows * p.n; i += kRows * 4) {
-      float x[4];
-      if (i + 3 < rows * p.n) {
+    const float* src = logits + t0 * N;  // rows N values from a 16-byte border
+    if (N % 4 == 0) {
+      for (int i = threadIdx.x * 4; i < rows * N; i += 8 * kRows) {
         const float4 f = __ldg(reinterpret_cast<const float4*>(src + i));
-        x[0] = f.x;
-        x[1] = f.y;
-        x[2] = f.z;
-        x[3] = f.w;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = i + j < rows * p.n ? __ldg(src + i + j) : 0.f;
+        const int r = (int)__umulhi(i, magic);
+        float* dst = tile + (i - r * N) * S + r;
+        dst[0] = f.x;
+        dst[S] = f.y;
+        dst[2 * S] = f.z;
+        dst[3 * S] = f.w;
       }
-      int r = p.n == 1 ? i : (int)__umulhi(i, magic), c = i - r * p.n;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (r < rows) tile[r * stride + c] = x[j];
-        if (++c == p.n) {
-          c = 0;
-          ++r;
-        }
+    } else {
+      for (int i = threadIdx.x; i < rows * N; i += 2 * kRows) {
+        const int r = N == 1 ? i : (int)__umulhi(i, magic);
+        tile[(i - r * N) * S + r] = __ldg(src + i);
       }
     }
     __syncthreads();
+    // Rows behind the last: whatever lies in their columns is computed with and not written.
     const bool live = tid < rows;
     const int64_t t = t0 + tid;
-    const float* row = tile + (live ? tid : 0) * stride;
+    float* col = tile + tid;                                  // expert e of this row at col[e S]
+    const float* row = logits + (t0 + (live ? tid : 0)) * N;  // the same in memory
     float top = -FLT_MAX, total = 0.f;
     if (!SIGMOID && !(BY_LOGIT && (p.renormalise || p.sigmoid))) {
-      for (int e = 0; e < p.n; ++e) top = fmaxf(top, there(row[e]) ? fminf(row[e], FLT_MAX) : -FLT_MAX);
-      float part[8] = {};
-      for (int e = 0; e < p.n; e += 8)
+      const int e0 = half ? (N + 1) / 2 : 0, e1 = half ? N : (N + 1) / 2;
+#pragma unroll 8
+      for (int e = e0; e < e1; ++e) top = fmaxf(top, there(col[e * S]) ? fminf(col[e * S], FLT_MAX) : -FLT_MAX);
+      swap[half * kRows + tid] = top;
+      __syncthreads();
+      top = fmaxf(top, swap[(1 - half) * kRows + tid]);
+      float part[4] = {};
+      for (int e = e0; e < e1; e += 4)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float l = e + j < p.n ? row[e + j] : -FLT_MAX;
+        for (int j = 0; j < 4; ++j) {
+          const float l = e + j < e1 ? col[(e + j) * S] : -FLT_MAX;
           part[j] += there(l) ? __expf(fminf(l, FLT_MAX) - top) : 0.f;
         }
-      total = ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
+      total = (part[0] + part[1]) + (part[2] + part[3]);
+      __syncthreads();
+      swap[half * kRows + tid] = total;
+      __syncthreads();
+      total = swap[tid] + swap[kRows + tid];
+      __syncthreads();
     }
     const float over = total > 0.f ? 1.f / total : 0.f;
-    auto value = [&](int e) {  // what is compared; -inf where the expert is out
-      const float l = row[e];
+    auto value = [&](float l, float b) {  // what is compared; -inf where the expert is out
       if (BY_LOGIT) return there(l) ? fminf(l, FLT_MAX) : -INFINITY;
       const float s = SIGMOID ? quick_sigmoid(l) : __expf(fminf(l, FLT_MAX) - top) * over;
-      return there(l) ? fmaxf(s + sb[e], -INFINITY) : -INFINITY;  // fmaxf drops a NaN
+      return there(l) ? s + b : -INFINITY;
     };
+    const float wide = 2.f * base;  // bound on the error of a difference of two values, with 2^-23 of each
+    auto apart = [&](float a, float b) { return BY_LOGIT ? a > b : a - b > wide + 1.2e-7f * (fabsf(a) + fabsf(b)); };
     bool doubt = false;
     unsigned kept = 1;
+    int key[K + 1];
+#pragma unroll
+    for (int j = 0; j <= K; ++j) key[j] = INT_MIN;
+    auto insert = [&](int x) {
+#pragma unroll
+      for (int j = 0; j <= K; ++j) {
+        const int a = max(x, key[j]);
+        x = min(x, key[j]);
+        key[j] = a;
+      }
+    };
+    auto clear_gates = [&]() {  // a warp writes 32 rows of one expert
+      float* out = gates + t0;
+      if (live)
+#pragma unroll 4
+        for (int e = 0; e < N; ++e, out += ld) out[tid] = 0.f;
+    };
     if (p.groups > 1) {
+      // the best two of every group, of each half
       for (int g = 0; g < p.groups; ++g) {
         float b1 = -INFINITY, b2 = -INFINITY;
-        for (int i = 0; i < size; ++i) {
-          const float v = value(g * size + i);
+        float* c = col + g * size * S;
+        const float* b = sb + g * size;
+#pragma unroll 4
+        for (int i = from; i < to; ++i) {
+          const float v = value(c[i * S], b[i]);
+          c[i * S] = v;  // from here on the tile holds the values
           b2 = fmaxf(b2, fminf(b1, v));
           b1 = fmaxf(b1, v);
         }
-        gsc[g * kRows + tid] = p.group_best == 2 && b2 > -INFINITY ? b1 + b2 : b1;
+        float* at = swap + 2 * g * kRows + tid;
+        if (half) {
+          at[0] = b1;
+          at[kRows] = b2;
+        } else {
+          at[2 * p.groups * kRows] = b1;
+          at[(2 * p.groups + 1) * kRows] = b2;
+        }
       }
-      kept = 0;
-      float last = INFINITY;
-      for (int r = 0; r < p.top_groups; ++r) {
-        float best = -INFINITY;
-        int at = -1;
+      __syncthreads();
+      if (half) {
+        if (gates) clear_gates();
+      } else {
         for (int g = 0; g < p.groups; ++g) {
-          const float x = gsc[g * kRows + tid];
-          if (!(kept >> g & 1) && x > best) {
-            best = x;
-            at = g;
+          float* at = swap + 2 * g * kRows + tid;
+          const float a1 = at[0], a2 = at[kRows], c1 = at[2 * p.groups * kRows], c2 = at[(2 * p.groups + 1) * kRows];
+          const float b1 = fmaxf(a1, c1), b2 = fmaxf(fminf(a1, c1), fmaxf(a2, c2));
+          at[0] = p.group_best == 2 && b2 > -INFINITY ? b1 + b2 : b1;
+        }
+        kept = 0;
+        float last = INFINITY;
+        for (int r = 0; r < p.top_groups; ++r) {
+          float best = -INFINITY;
+          int at = -1;
+#pragma unroll 4
+          for (int g = 0; g < p.groups; ++g) {
+            const float x = swap[2 * g * kRows + tid];
+            if (x > best) {
+              best = x;
+              at = g;
+            }
+          }
+          if (at >= 0) {
+            kept |= 1u << at;
+            last = best;
+            swap[2 * at * kRows + tid] = -INFINITY;
           }
         }
-        if (at >= 0) {
-          kept |= 1u << at;
-          last = best;
-        }
+        float next = -INFINITY;
+#pragma unroll 4
+        for (int g = 0; g < p.groups; ++g) next = fmaxf(next, swap[2 * g * kRows + tid]);
+        doubt = next > -INFINITY && !(last - next > 2.f * wide + 2.4e-7f * (fabsf(last) + fabsf(next)));
+        skept[tid] = kept;
       }
-      float next = -INFINITY;
-      for (int g = 0; g < p.groups; ++g)
-        if (!(kept >> g & 1)) next = fmaxf(next, gsc[g * kRows + tid]);
-      doubt = next > -INFINITY && !(last - next > 4.f * base + 2.4e-7f * (fabsf(last) + fabsf(next)));
+      __syncthreads();
+      kept = skept[tid];
+      for (unsigned left = kept; left; left &= left - 1) {
+        const int e0 = (__ffs(left) - 1) * size;
+        const float* c = col + e0 * S;
+#pragma unroll 4
+        for (int i = from; i < to; ++i) insert(key_of(c[i * S], e0 + i, mask));
+      }
+    } else {
+#pragma unroll 4
+      for (int e = from; e < to; ++e) insert(key_of(value(col[e * S], sb[e]), e, mask));
+      if (half && gates) clear_gates();
     }
+    if (half) {
+#pragma unroll
+      for (int j = 0; j <= K; ++j) swap[j * kRows + tid] = __int_as_float(key[j]);
+    }
+    __syncthreads();
+    if (half) continue;  // the next round's first barrier waits for the other half
+#pragma unroll
+    for (int j = 0; j <= K; ++j) insert(__float_as_int(swap[j * kRows + tid]));
+    // the value behind a key, as it was compared
+    auto held = [&](int k, int& e) {
+      e = mask - (k & mask);
+      const bool some = k != INT_MIN;
+      if (!some) e = 0;
+      const float v = p.groups > 1 ? col[e * S] : value(col[e * S], sb[e]);
+      return some ? v : -INFINITY;
+    };
     float val[K + 1];
     int idx[K + 1];
 #pragma unroll
-    for (int j = 0; j <= K; ++j) {
-      val[j] = -INFINITY;
-      idx[j] = -1;
-    }
-    for (unsigned left = kept; left; left &= left - 1) {
-      const int e0 = (__ffs(left) - 1) * size;
-      for (int i = 0; i < size; ++i) {
-        float v = value(e0 + i);
-        int at = e0 + i;
-        if (v > val[K]) {
-          bool up = false;  // from its place on, all move down by one: equal ones keep their order
+    for (int j = 0; j <= K; ++j) val[j] = held(key[j], idx[j]);
+    const float outside = key[K] != INT_MIN ? key_top(key[K], mask) : -INFINITY;  // no smaller key has more
 #pragma unroll
-          for (int j = 0; j <= K; ++j) {
-            up |= v > val[j];
-            const float a = up ? v : val[j];
-            const int b = up ? at : idx[j];
-            v = up ? val[j] : v;
-            at = up ? idx[j] : at;
-            val[j] = a;
-            idx[j] = b;
-          }
-        }
+    for (int j = K; j > 0; --j)  // neighbours that the keys' cut bits put the wrong way round
+      if (val[j] > val[j - 1]) {
+        const float a = val[j];
+        val[j] = val[j - 1];
+        val[j - 1] = a;
+        const int b = idx[j];
+        idx[j] = idx[j - 1];
+        idx[j - 1] = b;
       }
-    }
-    // close decisions
-    auto apart = [&](float a, float b) { return BY_LOGIT ? a > b : a - b > 2.f * base + 1.2e-7f * (fabsf(a) + fabsf(b)); };
     bool close = false;
+    float lastv = -INFINITY;
+    int lastid = -1;
 #pragma unroll
     for (int j = 0; j < K; ++j)
-      if (j < p.k && val[j + 1] > -INFINITY && !apart(val[j], val[j + 1])) close = true;
-    if (close && !doubt && !BY_LOGIT) {
-      // equal logits and biases are in their right order already
-      int lastid = -1;
-      float lastv = 0.f;
+      if (j < p.k && val[j] > -INFINITY) {
+        close |= val[j + 1] > -INFINITY && !apart(val[j], val[j + 1]);
+        lastv = val[j];
+        lastid = idx[j];
+      }
+    // Experts behind the last key: at most `outside`.  (Where fewer than k are
+    // left, the list holds them all and what is behind is -inf.)
+    close |= lastid >= 0 && outside > -INFINITY && val[K] > -INFINITY && !apart(lastv, outside);
+    if (close && !doubt) {
 #pragma unroll
-      for (int j = 0; j < K; ++j)
-        if (j < p.k && idx[j] >= 0) {
-          if (j + 1 < p.k && idx[j + 1] >= 0 && !apart(val[j], val[j + 1]))
-            doubt |= !(row[idx[j]] == row[idx[j + 1]] && sb[idx[j]] == sb[idx[j + 1]]);
-          lastid = idx[j];
-          lastv = val[j];
-        }
+      for (int j = 0; j + 1 < K; ++j)
+        if (j + 1 < p.k && val[j + 1] > -INFINITY && !apart(val[j], val[j + 1]))
+          doubt |= !(__ldg(row + idx[j]) == __ldg(row + idx[j + 1]) && sb[idx[j]] == sb[idx[j + 1]] && idx[j] < idx[j + 1]);
+      const float ll = __ldg(row + lastid), lb = sb[lastid];
       for (unsigned left = kept; left; left &= left - 1) {
         const int e0 = (__ffs(left) - 1) * size;
-        for (int i = 0; i < size; ++i) {
-          const int e = e0 + i;
-          const float v = value(e);
+        for (int e = e0; e < e0 + size; ++e) {
+          const float l = __ldg(row + e);
+          const float v = value(l, sb[e]);
           bool chosen = false;
 #pragma unroll
           for (int j = 0; j < K; ++j) chosen |= j < p.k && idx[j] == e;
-          if (!chosen && v > -INFINITY && !apart(lastv, v)) doubt |= !(row[e] == row[lastid] && sb[e] == sb[lastid]);
+          if (!chosen && v > -INFINITY && !apart(lastv, v)) doubt |= !(l == ll && sb[e] == lb && lastid < e);
         }
       }
     }
@@ -396,10 +492,12 @@ __global__ void __launch_bounds__(kRows) route_thread_kernel(RouteSpec p, int64_
       float m = -FLT_MAX, sum = 0.f;
 #pragma unroll
       for (int j = 0; j < K; ++j) {
-        if (j >= p.k) idx[j] = -1;
-        w[j] = idx[j] >= 0 ? fminf(row[max(idx[j], 0)], FLT_MAX) : 0.f;
-        if (idx[j] >= 0) m = fmaxf(m, w[j]);
+        if (j >= p.k || !(val[j] > -INFINITY)) idx[j] = -1;
+        w[j] = idx[j] < 0 ? 0.f : fminf(p.groups > 1 ? __ldg(row + idx[j]) : col[idx[j] * S], FLT_MAX);
       }
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        if (idx[j] >= 0) m = fmaxf(m, w[j]);
       if (SIGMOID || (BY_LOGIT && p.sigmoid)) {
         m = p.renormalise ? fminf(m, 0.f) : 0.f;
 #pragma unroll
@@ -419,30 +517,36 @@ __global__ void __launch_bounds__(kRows) route_thread_kernel(RouteSpec p, int64_
 #pragma unroll
       for (int j = 0; j < K; ++j) w[j] = idx[j] >= 0 ? w[j] * f : 0.f;
     }
-    if (live && !doubt) {
-#pragma unroll
-      for (int j = 0; j < K; ++j)
-        if (j < p.k) {
-          if (ids) ids[t * p.k + j] = idx[j];
-          if (weights) weights[t * p.k + j] = w[j];
-          if (counts && idx[j] >= 0) atomicAdd(hist + idx[j], 1);
-        }
-    }
-    if (gates && live) {
-      for (int e = 0; e < p.n; ++e) gates[(int64_t)e * ld + t] = 0.f;  // a warp writes 32 rows of one expert
+    if (live) {
       if (!doubt) {
+        if (K % 4 == 0 && p.k == K) {
+#pragma unroll
+          for (int j = 0; j + 3 < K; j += 4) {
+            if (ids) *reinterpret_cast<int4*>(ids + t * K + j) = make_int4(idx[j], idx[j + 1], idx[j + 2], idx[j + 3]);
+            if (weights) *reinterpret_cast<float4*>(weights + t * K + j) = make_float4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < K; ++j)
+            if (j < p.k) {
+              if (ids) ids[t * p.k + j] = idx[j];
+              if (weights) weights[t * p.k + j] = w[j];
+            }
+        }
 #pragma unroll
         for (int j = 0; j < K; ++j)
-          if (idx[j] >= 0) gates[(int64_t)idx[j] * ld + t] = w[j];
+          if (idx[j] >= 0) {
+            if (gates) gates[(int64_t)idx[j] * ld + t] = w[j];
+            if (counts) atomicAdd(hist + idx[j], 1);
+          }
       }
     }
     __syncwarp();
     for (unsigned left = __ballot_sync(kAll, doubt); left; left &= left - 1) {
-      const int r = __ffs(left) - 1;
-      const int64_t tr = t0 + (tid & ~31) + r;
+      const int64_t tr = t0 + (tid & ~31) + __ffs(left) - 1;
       int id;
       float wj;
-      route_row<kThreadExperts / 32>(p, tile + ((tid & ~31) + r) * stride, bias, &id, &wj);
+      route_row<kThreadExperts / 32>(p, logits + tr * N, bias, &id, &wj);
       if (lane < p.k) {
         if (ids) ids[tr * p.k + lane] = id;
         if (weights) weights[tr * p.k + lane] = wj;
@@ -455,14 +559,16 @@ __global__ void __launch_bounds__(kRows) route_thread_kernel(RouteSpec p, int64_
   }
   if (counts) {
     __syncthreads();
-    for (int e = tid; e < p.n; e += kRows)
+    for (int e = threadIdx.x; e < N; e += 2 * kRows)
       if (hist[e]) atomicAdd(counts + e, hist[e]);
   }
 }
 
 // ---- backward, one thread a row: the gradient is built in shared memory and
-// written in whole lines
+// written in whole lines.  A row's ids, logits and gradients are read at once
+// (K places; the gates' gradient of a chosen expert is one 32-byte sector).
 
+template <int K, bool EVERY>  // EVERY: the softmax's sum reaches every logit
 __global__ void __launch_bounds__(kRows) route_backward_kernel(RouteSpec p, int64_t n, const float* __restrict__ logits,
                                                                const int32_t* __restrict__ ids,
                                                                const float* __restrict__ grad_weights,
@@ -470,89 +576,106 @@ __global__ void __launch_bounds__(kRows) route_backward_kernel(RouteSpec p, int6
                                                                float* __restrict__ grad_logits, unsigned magic) {
   grid_dependency_wait();
   grid_launch_dependents();
-  extern __shared__ float smem[];
-  const int stride = p.n | 1, tid = threadIdx.x, R = blockDim.x;
-  const bool every = !p.sigmoid && !p.renormalise;  // the softmax's sum reaches every logit
+  extern __shared__ float4 smem4[];
+  float* smem = reinterpret_cast<float*>(smem4);
+  const int N = p.n, stride = EVERY ? N | 1 : N, tid = threadIdx.x, R = blockDim.x;
   for (int64_t t0 = (int64_t)blockIdx.x * R; t0 < n; t0 += (int64_t)gridDim.x * R) {
     const int rows = (int)min((int64_t)R, n - t0);
+    const bool live = tid < rows;
+    const int64_t t = t0 + tid;
+    int id[K];
+    float l[K], d[K];
+#pragma unroll
+    for (int j = 0; j < K; ++j) id[j] = live && j < p.k ? __ldg(ids + t * p.k + j) : -1;
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      const bool in = (unsigned)id[j] < (unsigned)N;
+      l[j] = in ? __ldg(logits + t * N + id[j]) : -FLT_MAX;
+      d[j] = in && grad_gates ? __ldg(grad_gates + (int64_t)id[j] * ld + t) : 0.f;
+      if (in && grad_weights) d[j] += __ldg(grad_weights + t * p.k + j);
+    }
     __syncthreads();
-    if (every) {
-      const float* src = logits + t0 * p.n;
-      for (int i = tid; i < rows * p.n; i += R) {
-        const int r = p.n == 1 ? i : (int)__umulhi(i, magic);
-        smem[r * stride + i - r * p.n] = __ldg(src + i);
+    if (EVERY) {
+      const float* src = logits + t0 * N;
+      for (int i = tid; i < rows * N; i += R) {
+        const int r = N == 1 ? i : (int)__umulhi(i, magic);
+        smem[r * stride + i - r * N] = __ldg(src + i);
       }
     } else {
-      for (int i = tid; i < rows * stride; i += R) smem[i] = 0.f;
+      for (int i = tid; i < (rows * N + 3) / 4; i += R) smem4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     __syncthreads();
-    if (tid < rows) {
-      const int64_t t = t0 + tid;
-      const float* row = logits + t * p.n;
+    if (live) {
       float* out = smem + tid * stride;
-      auto chosen = [&](int j, float& l, float& d) {
-        const int id = __ldg(ids + t * p.k + j);
-        if ((unsigned)id >= (unsigned)p.n) return -1;
-        l = __ldg(row + id);
-        if (!there(l)) return -1;
-        l = fminf(l, FLT_MAX);
-        d = (grad_weights ? __ldg(grad_weights + t * p.k + j) : 0.f) +
-            (grad_gates ? __ldg(grad_gates + (int64_t)id * ld + t) : 0.f);
-        return id;
-      };
-      float l, d;
-      if (every) {
-        float top = -FLT_MAX, total = 0.f, dot = 0.f;
-        for (int e = 0; e < p.n; ++e) top = fmaxf(top, there(out[e]) ? fminf(out[e], FLT_MAX) : -FLT_MAX);
-        for (int e = 0; e < p.n; ++e) total += there(out[e]) ? expf(fminf(out[e], FLT_MAX) - top) : 0.f;
-        const float over = total > 0.f ? 1.f / total : 0.f;
-        for (int j = 0; j < p.k; ++j)
-          if (chosen(j, l, d) >= 0) dot = fmaf(d, expf(l - top) * over, dot);
-        dot *= p.scale;
-        for (int e = 0; e < p.n; ++e)
-          out[e] = there(out[e]) ? -(expf(fminf(out[e], FLT_MAX) - top) * over) * dot : 0.f;
-        for (int j = 0; j < p.k; ++j) {
-          const int id = chosen(j, l, d);
-          if (id >= 0) out[id] += p.scale * d * (expf(l - top) * over);
-        }
-      } else {
-        float m = p.sigmoid ? 0.f : -FLT_MAX, sum = 0.f, dot = 0.f;
-        if (p.renormalise) {
-          float top = -FLT_MAX;
-          for (int j = 0; j < p.k; ++j)
-            if (chosen(j, l, d) >= 0) top = fmaxf(top, l);
-          m = p.sigmoid ? fminf(top, 0.f) : top;
-        }
-        // a score relative to exp(m)
-        auto score = [&](float x) {
-          if (!p.sigmoid) return expf(x - m);
-          return x > 0.f || !p.renormalise ? 1.f / (1.f + expf(-x)) : expf(x - m) / (1.f + expf(x));
-        };
-        if (p.renormalise) {
-          for (int j = 0; j < p.k; ++j)
-            if (chosen(j, l, d) >= 0) {
-              const float s = score(l);
-              sum += s;
-              dot = fmaf(d, s, dot);
-            }
-          sum = sum > 0.f ? 1.f / sum : 0.f;
-          dot *= sum;
-        }
-        for (int j = 0; j < p.k; ++j) {
-          const int id = chosen(j, l, d);
-          if (id < 0) continue;
-          float x = p.scale * score(l);
-          x *= p.renormalise ? sum * (d - dot) : d;
-          if (p.sigmoid) x *= 1.f / (1.f + expf(l));
-          out[id] += x;
-        }
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        if (!there(l[j])) id[j] = -1;  // out of range, out for the row, or NaN
+        l[j] = fminf(l[j], FLT_MAX);
       }
+      if (EVERY) {
+        float top = -FLT_MAX, total = 0.f, dot = 0.f;
+#pragma unroll 8
+        for (int e = 0; e < N; ++e) top = fmaxf(top, there(out[e]) ? fminf(out[e], FLT_MAX) : -FLT_MAX);
+#pragma unroll 4
+        for (int e = 0; e < N; ++e) {
+          const float x = there(out[e]) ? expf(fminf(out[e], FLT_MAX) - top) : 0.f;
+          out[e] = x;
+          total += x;
+        }
+        const float over = total > 0.f ? 1.f / total : 0.f;
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+          if (id[j] >= 0) {
+            d[j] *= p.scale * (out[id[j]] * over);
+            dot += d[j];
+          }
+        dot *= over;
+#pragma unroll 4
+        for (int e = 0; e < N; ++e) out[e] *= -dot;
+      } else {
+        float m = 0.f, sum = 0.f, dot = 0.f;
+        if (p.renormalise) {
+          m = -FLT_MAX;
+#pragma unroll
+          for (int j = 0; j < K; ++j)
+            if (id[j] >= 0) m = fmaxf(m, l[j]);
+          if (p.sigmoid) m = fminf(m, 0.f);
+        }
+        // scores, the renormalised ones relative to exp(m); with one minus the sigmoid
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+          if (id[j] >= 0) {
+            const float x = l[j];
+            float sj;
+            if (!p.sigmoid) {
+              sj = expf(x - m);
+              l[j] = sj;
+            } else {
+              sj = x > 0.f || !p.renormalise ? 1.f / (1.f + expf(-x)) : expf(x - m) / (1.f + expf(x));
+              l[j] = sj / (1.f + expf(x));  // s (1 - s)
+            }
+            sum += sj;
+            dot = fmaf(d[j], sj, dot);
+          }
+        const float over = p.renormalise ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
+        const float mean = p.renormalise ? dot * over : 0.f;
+#pragma unroll
+        for (int j = 0; j < K; ++j) d[j] = p.scale * over * l[j] * (d[j] - mean);
+      }
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        if (id[j] >= 0) out[id[j]] += d[j];
     }
     __syncthreads();
-    float* dst = grad_logits + t0 * p.n;
-    for (int i = tid; i < rows * p.n; i += R) {
-      const int r = p.n == 1 ? i : (int)__umulhi(i, magic);
-      dst[i] = smem[r * stride + i - r * p.n];
+    float* dst = grad_logits + t0 * N;
+    if (EVERY) {
+      for (int i = tid; i < rows * N; i += R) {
+        const int r = N == 1 ? i : (int)__umulhi(i, magic);
+        dst[i] = smem[r * stride + i - r * N];
+      }
+    } else {
+      for (int i = tid; i < rows * N / 4; i += R) reinterpret_cast<float4*>(dst)[i] = smem4[i];
+      for (int i = (rows * N & ~3) + tid; i < rows * N; i += R) dst[i] = smem[i];
     }
   }
 }
@@ -607,13 +730,25 @@ cudaError_t forward_warps(const RouteSpec& p, int64_t n, const float* logits, co
 template <int K>
 cudaError_t forward_threads(const RouteSpec& p, int64_t n, const float* logits, const float* bias, const RouteOut& o,
                             cudaStream_t s) {
-  const size_t shared = sizeof(float) * ((size_t)kRows * (p.n | 1) + 2 * p.n + (p.groups > 1 ? p.groups * kRows : 0));
-  const int64_t grid = std::min<int64_t>((n + kRows - 1) / kRows, kSms * 8);
+  const int swap_rows = std::max(K + 1, p.groups > 1 ? 4 * p.groups : 2);
+  const size_t shared = sizeof(float) * ((size_t)(kRows + 1) * p.n + 2 * p.n + (size_t)(1 + swap_rows) * kRows);
+  const int64_t grid = std::min<int64_t>((n + kRows - 1) / kRows, kSms * 64);
   auto kernel = !bias && p.groups == 1 ? route_thread_kernel<K, false, true>
                 : p.sigmoid            ? route_thread_kernel<K, true, false>
                                        : route_thread_kernel<K, false, false>;
-  return launch_dependent(kernel, grid, kRows, shared, s, p, n, logits, bias, o.ids, o.weights, o.gates, o.ld,
+  return launch_dependent(kernel, grid, 2 * kRows, shared, s, p, n, logits, bias, o.ids, o.weights, o.gates, o.ld,
                           o.counts, divide_by(p.n));
+}
+
+template <int K>
+cudaError_t backward_rows(const RouteSpec& p, int64_t n, const float* logits, const int32_t* ids, const float* gw,
+                          const float* gg, int64_t ld, float* out, cudaStream_t s) {
+  const unsigned rows = p.n <= 64 ? kRows : p.n <= 256 ? 64 : 32;  // tiles of 33 to 66 KB
+  const int64_t grid = std::min<int64_t>((n + rows - 1) / rows, kSms * 64);
+  const bool every = !p.sigmoid && !p.renormalise;
+  return launch_dependent(every ? route_backward_kernel<K, true> : route_backward_kernel<K, false>, grid, rows,
+                          sizeof(float) * rows * (every ? p.n | 1 : p.n), s, p, n, logits, ids, gw, gg, ld, out,
+                          divide_by(p.n));
 }
 
 cudaError_t launch_forward(const RouteSpec& p, int64_t n, const float* logits, const float* bias, const RouteOut& o,
@@ -704,11 +839,12 @@ cgtp_status cgtp_router_backward(cgtp_router router, int64_t n, const float* log
                         (const void*)grad_logits})
     if (q && !aligned16(q)) return fail(CGTP_ERR_ALIGN, "arrays must be 16-byte aligned");
   const RouteSpec& p = router->p;
-  const unsigned rows = p.n <= 64 ? kRows : p.n <= 256 ? 64 : 32;  // tiles of 33 to 66 KB
-  const int64_t grid = std::min<int64_t>((n + rows - 1) / rows, kSms * 12);
-  CGTP_CUDA_TRY(launch_dependent(route_backward_kernel, grid, rows, sizeof(float) * rows * (p.n | 1),
-                                 (cudaStream_t)stream, p, n, logits, ids, grad_weights, grad_gates, ld, grad_logits,
-                                 divide_by(p.n)));
+  auto run = p.k == 1   ? backward_rows<1>
+             : p.k == 2 ? backward_rows<2>
+             : p.k <= 4 ? backward_rows<4>
+             : p.k <= 8 ? backward_rows<8>
+                        : backward_rows<kMaxK>;
+  CGTP_CUDA_TRY(run(p, n, logits, ids, grad_weights, grad_gates, ld, grad_logits, (cudaStream_t)stream));
   return CGTP_OK;
 }
 
