@@ -37,6 +37,9 @@ __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// 1 / (1 + e^-l); CUDA's fast exponential and division
+__device__ __forceinline__ float quick_sigmoid(float l) { return __fdividef(1.f, 1.f + __expf(-l)); }
+
 template <class X>
 __device__ __forceinline__ X warp_sum(X v) {
 #pragma unroll
@@ -174,6 +177,165 @@ __device__ __forceinline__ void route_row(const RouteSpec& p, const float* row, 
   *w_out = (float)((double)p.scale * w);
 }
 
+// ---- one row by one warp in FP32: false where two compared values are closer
+// than their error (then route_row decides)
+
+__device__ __forceinline__ int ordered(float v) {  // an integer in the order of the values
+  const int i = __float_as_int(v);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+
+// The error of a compared value.
+//   sigmoid: 1 / (1 + __expf(-l)): the exponent's rounding and the function's error
+//   give s (1 - s) (|l| 2^-24 + 2^-22) < 8e-8, the division 2 ulp: |ds| < 2e-7
+//   softmax: exp(l - top) off by < 2.7e-7 in the same way; the sum's relative
+//   error, in eight partial sums at least, (n / 8 + 4) 2^-24, is common to all
+//   scores <= 1
+//   adding the bias rounds by 2^-24 |v|
+// A difference of two is off by twice that; a group's score adds two values.
+__device__ __forceinline__ float value_error(int n, bool sigmoid) {
+  return sigmoid ? 4e-7f : 6e-7f + (float)(n / 8 + 4) * 6e-8f;
+}
+
+template <int PER>
+__device__ __forceinline__ bool route_row_fast(const RouteSpec& p, const float* row, const float* bias, int* id_out,
+                                               float* w_out) {
+  constexpr int kLow = INT_MIN;
+  const int lane = threadIdx.x & 31, size = p.n / p.groups;
+  const bool by_logit = !bias && p.groups == 1;
+  const int none = ordered(-INFINITY);
+  float l[PER];
+  int v[PER], best = kLow;
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    const int e = q * 32 + lane;
+    l[q] = e < p.n ? fminf(__ldg(row + e), FLT_MAX) : -FLT_MAX;  // fminf drops a NaN ...
+    if (e < p.n && !there(__ldg(row + e))) l[q] = -FLT_MAX;      // ... which rules the expert out
+    best = max(best, ordered(l[q]));
+  }
+  const float top = unordered(__reduce_max_sync(kAll, best));
+  float s[PER], total = 0.f;
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    s[q] = !there(l[q]) ? 0.f : p.sigmoid ? quick_sigmoid(l[q]) : __expf(l[q] - top);
+    total += s[q];
+  }
+  float over = 1.f;
+  if (!p.sigmoid) {
+    total = warp_sum(total);
+    over = total > 0.f ? 1.f / total : 0.f;
+  }
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    v[q] = none;
+    if (there(l[q])) {
+      const float b = bias ? __ldg(bias + q * 32 + lane) : 0.f;
+      const float x = by_logit ? l[q] : s[q] * over + b;
+      if (x > -INFINITY) v[q] = ordered(x);
+    }
+  }
+  const float wide = 2.f * value_error(p.n, p.sigmoid);
+  auto apart = [&](float a, float b) { return by_logit ? a > b : a - b > wide + 1.2e-7f * (fabsf(a) + fabsf(b)); };
+  // the largest value of the experts from..to - 1 and its lowest index, which is then taken out
+  auto take = [&](int from, int to, int& at) {
+    int m = none;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const int e = q * 32 + lane;
+      if (e >= from && e < to) m = max(m, v[q]);
+    }
+    m = __reduce_max_sync(kAll, m);
+    int i = INT_MAX;
+#pragma unroll
+    for (int q = PER - 1; q >= 0; --q) {
+      const int e = q * 32 + lane;
+      if (e >= from && e < to && v[q] == m) i = e;
+    }
+    at = __reduce_min_sync(kAll, i);
+    return unordered(m);
+  };
+  auto drop = [&](int at) {
+#pragma unroll
+    for (int q = 0; q < PER; ++q)
+      if (q * 32 + lane == at) v[q] = none;
+  };
+  if (p.groups > 1) {
+    float mine = -INFINITY;  // lane g: the score of group g
+    for (int g = 0; g < p.groups; ++g) {
+      int at, m = none;
+      const float b1 = take(g * size, (g + 1) * size, at);
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        const int e = q * 32 + lane;
+        if (e >= g * size && e < (g + 1) * size && e != at) m = max(m, v[q]);
+      }
+      float sum = b1;
+      if (p.group_best == 2) {
+        const float b2 = unordered(__reduce_max_sync(kAll, m));
+        if (b2 > -INFINITY) sum += b2;
+      }
+      if (lane == g) mine = sum;
+    }
+    unsigned kept = 0;
+    float last = INFINITY;
+    int score = ordered(mine);
+    for (int r = 0; r < p.top_groups; ++r) {
+      const int m = __reduce_max_sync(kAll, score);
+      if (m == none) break;
+      const int at = __ffs(__ballot_sync(kAll, score == m)) - 1;
+      kept |= 1u << at;
+      last = unordered(m);
+      if (lane == at) score = none;
+    }
+    const float next = unordered(__reduce_max_sync(kAll, score));
+    if (next > -INFINITY && !(last - next > 2.f * wide + 2.4e-7f * (fabsf(last) + fabsf(next)))) return false;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const int e = q * 32 + lane;
+      if (e < p.n && !(kept >> (e / size) & 1)) v[q] = none;
+    }
+  }
+  // equal logits and biases: in their right order already
+  auto same = [&](int a, int b) {
+    return __ldg(row + a) == __ldg(row + b) && (!bias || __ldg(bias + a) == __ldg(bias + b));
+  };
+  int id = -1, before = -1;
+  float last = INFINITY;
+  for (int j = 0; j < p.k; ++j) {
+    int at;
+    const float x = take(0, p.n, at);
+    if (!(x > -INFINITY)) break;
+    if (before >= 0 && !apart(last, x) && !same(before, at)) return false;
+    drop(at);
+    if (lane == j) id = at;
+    before = at;
+    last = x;
+  }
+  for (;;) {  // those not chosen
+    int at;
+    const float x = take(0, p.n, at);
+    if (!(x > -INFINITY) || before < 0 || apart(last, x)) break;
+    if (!same(before, at)) return false;
+    drop(at);
+  }
+  // weights, as in route_row
+  const float lj = id >= 0 ? fminf(__ldg(row + max(id, 0)), FLT_MAX) : 0.f;
+  float w = 0.f;
+  if (!p.renormalise) {
+    if (id >= 0) w = p.sigmoid ? 1.f / (1.f + expf(-lj)) : expf(lj - top) * over;
+  } else {
+    float m = unordered(__reduce_max_sync(kAll, id >= 0 ? ordered(lj) : kLow));
+    if (p.sigmoid) m = fminf(m, 0.f);
+    if (id >= 0) w = !p.sigmoid ? expf(lj - m) : lj > 0.f ? 1.f / (1.f + expf(-lj)) : expf(lj - m) / (1.f + expf(lj));
+    const float sum = warp_sum(w);
+    if (id >= 0) w /= sum;
+  }
+  *id_out = id;
+  *w_out = p.scale * w;
+  return true;
+}
+
 // ---- forward, one warp a row, eight rows a CTA (few rows, many experts, k > 8)
 
 template <int PER>
@@ -190,7 +352,7 @@ __global__ void __launch_bounds__(256) route_warp_kernel(RouteSpec p, int64_t n,
     if (t < n) {  // whole warps
       int id;
       float w;
-      route_row<PER>(p, logits + t * p.n, bias, &id, &w);
+      if (!route_row_fast<PER>(p, logits + t * p.n, bias, &id, &w)) route_row<PER>(p, logits + t * p.n, bias, &id, &w);
       if (lane < p.k) {
         if (ids) ids[t * p.k + lane] = id;
         if (weights) weights[t * p.k + lane] = w;
@@ -218,7 +380,6 @@ constexpr int kRows = 128;           // rows of a CTA's tile
 constexpr int kThreadExperts = 128;  // the widest row of this form
 constexpr int kThreadK = 8;
 
-__device__ __forceinline__ float quick_sigmoid(float l) { return __fdividef(1.f, 1.f + __expf(-l)); }
 
 // A key whose order as an integer is the value's, its low bits replaced so that of
 // equal values the lowest index is the largest; mask = 2^bits - 1 >= experts - 1.
@@ -236,17 +397,11 @@ __device__ __forceinline__ float key_top(int key, int mask) {
 }
 
 // A row's choice in FP32, by one thread.  Two compared values are off by at
-// most a bound against one another; where a decision is closer than that the row
-// is looked at again (two experts of equal logit and bias are in their right
-// order already) and, if that does not settle it, decided in 64 bits by the
-// whole warp.
-//   sigmoid: 1 / (1 + __expf(-l)): the exponent's rounding and the function's error
-//   give s (1 - s) (|l| 2^-24 + 2^-22) < 8e-8, the division 2 ulp: |ds| < 2e-7
-//   softmax: exp(l - top) off by < 2.7e-7 in the same way; the sum's relative
-//   error, eight partial sums, (n / 8 + 4) 2^-24, is common to all scores <= 1
-//   adding the bias rounds by 2^-24 |v|
-// and a group's score adds two such values.  The k + 1 best are found as integer
-// keys (two instructions a place and expert) that hold the index in their
+// most twice value_error against one another; where a decision is closer than that
+// the row is looked at again (two experts of equal logit and bias are in their
+// right order already) and, if that does not settle it, decided in 64 bits by the
+// whole warp.  The k + 1 best are found as integer keys (two instructions a
+// place and expert) that hold the index in their
 // low bits; the keys' order is put right from the values themselves.
 //
 // Two threads share a row, each with one half of every group: the second also
@@ -275,7 +430,7 @@ __global__ void __launch_bounds__(2 * kRows) route_thread_kernel(
   }
   int mask = 1;
   while (mask < N - 1) mask = 2 * mask + 1;
-  const float base = SIGMOID ? 4e-7f : 6e-7f + (float)(N / 8 + 4) * 6e-8f;
+  const float base = value_error(N, SIGMOID);
   const int size = N / p.groups, split = (size + 1) / 2;
   const int from = half ? split : 0, to = half ? size : split;  // this thread's part of a group
   for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < n; t0 += (int64_t)gridDim.x * kRows) {
@@ -564,21 +719,27 @@ __global__ void __launch_bounds__(2 * kRows) route_thread_kernel(
   }
 }
 
-// ---- backward, one thread a row: the gradient is built in shared memory and
-// written in whole lines.  A row's ids, logits and gradients are read at once
-// (K places; the gates' gradient of a chosen expert is one 32-byte sector).
+// ---- backward where only the chosen experts' logits have a gradient: one
+// thread a row; the gradient is built in shared memory and written in whole
+// lines.  A chosen expert's logit and gate gradient are one sector each, and an SM
+// holds few requests of one sector: where the row is not much longer than its
+// choices and the arrays are large, the whole rows are read and the places picked
+// in shared memory (172,050 x 64, k = 8: 79 us by single sectors, 41 us whole;
+// 21,828 x 24, k = 6: 4.5 us by single sectors, 5.6 us whole).
 
-template <int K, bool EVERY>  // EVERY: the softmax's sum reaches every logit
-__global__ void __launch_bounds__(kRows) route_backward_kernel(RouteSpec p, int64_t n, const float* __restrict__ logits,
-                                                               const int32_t* __restrict__ ids,
-                                                               const float* __restrict__ grad_weights,
-                                                               const float* __restrict__ grad_gates, int64_t ld,
-                                                               float* __restrict__ grad_logits, unsigned magic) {
+constexpr int64_t kWholeRows = 1 << 22;  // values of an array
+
+template <int K>
+__global__ void __launch_bounds__(kRows) route_chosen_backward_kernel(
+    RouteSpec p, int64_t n, const float* __restrict__ logits, const int32_t* __restrict__ ids,
+    const float* __restrict__ grad_weights, const float* __restrict__ grad_gates, int64_t ld,
+    float* __restrict__ grad_logits, unsigned magic) {
   grid_dependency_wait();
   grid_launch_dependents();
   extern __shared__ float4 smem4[];
   float* smem = reinterpret_cast<float*>(smem4);
-  const int N = p.n, stride = EVERY ? N | 1 : N, tid = threadIdx.x, R = blockDim.x;
+  const int N = p.n, tid = threadIdx.x, R = blockDim.x, odd = N | 1;
+  const bool whole = N <= 16 * p.k && n * N >= kWholeRows;
   for (int64_t t0 = (int64_t)blockIdx.x * R; t0 < n; t0 += (int64_t)gridDim.x * R) {
     const int rows = (int)min((int64_t)R, n - t0);
     const bool live = tid < rows;
@@ -587,96 +748,152 @@ __global__ void __launch_bounds__(kRows) route_backward_kernel(RouteSpec p, int6
     float l[K], d[K];
 #pragma unroll
     for (int j = 0; j < K; ++j) id[j] = live && j < p.k ? __ldg(ids + t * p.k + j) : -1;
-#pragma unroll
-    for (int j = 0; j < K; ++j) {
-      const bool in = (unsigned)id[j] < (unsigned)N;
-      l[j] = in ? __ldg(logits + t * N + id[j]) : -FLT_MAX;
-      d[j] = in && grad_gates ? __ldg(grad_gates + (int64_t)id[j] * ld + t) : 0.f;
-      if (in && grad_weights) d[j] += __ldg(grad_weights + t * p.k + j);
-    }
-    __syncthreads();
-    if (EVERY) {
-      const float* src = logits + t0 * N;
-      for (int i = tid; i < rows * N; i += R) {
-        const int r = N == 1 ? i : (int)__umulhi(i, magic);
-        smem[r * stride + i - r * N] = __ldg(src + i);
-      }
-    } else {
-      for (int i = tid; i < (rows * N + 3) / 4; i += R) smem4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    __syncthreads();
-    if (live) {
-      float* out = smem + tid * stride;
+    if (!whole) {
 #pragma unroll
       for (int j = 0; j < K; ++j) {
+        const bool in = (unsigned)id[j] < (unsigned)N;
+        l[j] = in ? __ldg(logits + t * N + id[j]) : -FLT_MAX;
+        d[j] = in && grad_gates ? __ldg(grad_gates + (int64_t)id[j] * ld + t) : 0.f;
+      }
+      __syncthreads();  // the tile of the round before is written out
+    } else {
+      __syncthreads();
+      if (grad_gates) {  // expert e of this row at smem[e R + tid]: only this thread's
+        const float* src = grad_gates + t0;
+        if (live)
+#pragma unroll 8
+          for (int e = 0; e < N; ++e, src += ld) smem[e * R + tid] = __ldg(src + tid);
+      }
+#pragma unroll
+      for (int j = 0; j < K; ++j) d[j] = (unsigned)id[j] < (unsigned)N && grad_gates ? smem[id[j] * R + tid] : 0.f;
+      __syncthreads();
+      const float* src = logits + t0 * N;
+      if (N % 4 == 0) {
+#pragma unroll 4
+        for (int i = tid * 4; i < rows * N; i += R * 4) {
+          const float4 f = __ldg(reinterpret_cast<const float4*>(src + i));
+          const int r = (int)__umulhi(i, magic);
+          float* dst = smem + r * odd + i - r * N;
+          dst[0] = f.x;
+          dst[1] = f.y;
+          dst[2] = f.z;
+          dst[3] = f.w;
+        }
+      } else {
+#pragma unroll 4
+        for (int i = tid; i < rows * N; i += R) {
+          const int r = N == 1 ? i : (int)__umulhi(i, magic);
+          smem[r * odd + i - r * N] = __ldg(src + i);
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < K; ++j) l[j] = (unsigned)id[j] < (unsigned)N ? smem[tid * odd + id[j]] : -FLT_MAX;
+      __syncthreads();
+    }
+    for (int i = tid; i < (rows * N + 3) / 4; i += R) smem4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncthreads();
+    if (live) {
+      float* out = smem + tid * N;
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        if ((unsigned)id[j] < (unsigned)N && grad_weights) d[j] += __ldg(grad_weights + t * p.k + j);
         if (!there(l[j])) id[j] = -1;  // out of range, out for the row, or NaN
         l[j] = fminf(l[j], FLT_MAX);
       }
-      if (EVERY) {
-        float top = -FLT_MAX, total = 0.f, dot = 0.f;
-#pragma unroll 8
-        for (int e = 0; e < N; ++e) top = fmaxf(top, there(out[e]) ? fminf(out[e], FLT_MAX) : -FLT_MAX);
-#pragma unroll 4
-        for (int e = 0; e < N; ++e) {
-          const float x = there(out[e]) ? expf(fminf(out[e], FLT_MAX) - top) : 0.f;
-          out[e] = x;
-          total += x;
-        }
-        const float over = total > 0.f ? 1.f / total : 0.f;
+      float m = 0.f, sum = 0.f, dot = 0.f;
+      if (p.renormalise) {
+        m = -FLT_MAX;
 #pragma unroll
         for (int j = 0; j < K; ++j)
-          if (id[j] >= 0) {
-            d[j] *= p.scale * (out[id[j]] * over);
-            dot += d[j];
-          }
-        dot *= over;
-#pragma unroll 4
-        for (int e = 0; e < N; ++e) out[e] *= -dot;
-      } else {
-        float m = 0.f, sum = 0.f, dot = 0.f;
-        if (p.renormalise) {
-          m = -FLT_MAX;
-#pragma unroll
-          for (int j = 0; j < K; ++j)
-            if (id[j] >= 0) m = fmaxf(m, l[j]);
-          if (p.sigmoid) m = fminf(m, 0.f);
-        }
-        // scores, the renormalised ones relative to exp(m); with one minus the sigmoid
-#pragma unroll
-        for (int j = 0; j < K; ++j)
-          if (id[j] >= 0) {
-            const float x = l[j];
-            float sj;
-            if (!p.sigmoid) {
-              sj = expf(x - m);
-              l[j] = sj;
-            } else {
-              sj = x > 0.f || !p.renormalise ? 1.f / (1.f + expf(-x)) : expf(x - m) / (1.f + expf(x));
-              l[j] = sj / (1.f + expf(x));  // s (1 - s)
-            }
-            sum += sj;
-            dot = fmaf(d[j], sj, dot);
-          }
-        const float over = p.renormalise ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
-        const float mean = p.renormalise ? dot * over : 0.f;
-#pragma unroll
-        for (int j = 0; j < K; ++j) d[j] = p.scale * over * l[j] * (d[j] - mean);
+          if (id[j] >= 0) m = fmaxf(m, l[j]);
+        if (p.sigmoid) m = fminf(m, 0.f);
       }
+      // scores, the renormalised ones relative to exp(m); with one minus the sigmoid
 #pragma unroll
       for (int j = 0; j < K; ++j)
-        if (id[j] >= 0) out[id[j]] += d[j];
+        if (id[j] >= 0) {
+          const float x = l[j];
+          float sj;
+          if (!p.sigmoid) {
+            sj = expf(x - m);
+            l[j] = sj;
+          } else {
+            sj = x > 0.f || !p.renormalise ? 1.f / (1.f + expf(-x)) : expf(x - m) / (1.f + expf(x));
+            l[j] = sj / (1.f + expf(x));  // s (1 - s)
+          }
+          sum += sj;
+          dot = fmaf(d[j], sj, dot);
+        }
+      const float over = p.renormalise ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
+      const float mean = p.renormalise ? dot * over : 0.f;
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        if (id[j] >= 0) out[id[j]] += p.scale * over * l[j] * (d[j] - mean);
     }
     __syncthreads();
     float* dst = grad_logits + t0 * N;
-    if (EVERY) {
-      for (int i = tid; i < rows * N; i += R) {
-        const int r = N == 1 ? i : (int)__umulhi(i, magic);
-        dst[i] = smem[r * stride + i - r * N];
-      }
-    } else {
-      for (int i = tid; i < rows * N / 4; i += R) reinterpret_cast<float4*>(dst)[i] = smem4[i];
-      for (int i = (rows * N & ~3) + tid; i < rows * N; i += R) dst[i] = smem[i];
+    for (int i = tid; i < rows * N / 4; i += R) reinterpret_cast<float4*>(dst)[i] = smem4[i];
+    for (int i = (rows * N & ~3) + tid; i < rows * N; i += R) dst[i] = smem[i];
+  }
+}
+
+// ---- backward of the softmax as it is, whose sum reaches every logit: L
+// lanes a row, lane i the experts i, i + L, ...; lane j also the row's j-th choice.
+
+template <int L, int PER>
+__global__ void __launch_bounds__(256) route_every_backward_kernel(
+    RouteSpec p, int64_t n, const float* __restrict__ logits, const int32_t* __restrict__ ids,
+    const float* __restrict__ grad_weights, const float* __restrict__ grad_gates, int64_t ld,
+    float* __restrict__ grad_logits) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  constexpr int rows = 256 / L;
+  const int lane = threadIdx.x & (L - 1), N = p.n;
+  for (int64_t t0 = (int64_t)blockIdx.x * rows; t0 < n; t0 += (int64_t)gridDim.x * rows) {  // whole CTAs
+    const int64_t t = t0 + threadIdx.x / L;
+    const bool live = t < n;
+    const float* row = logits + (live ? t : n - 1) * N;
+    int id = live && lane < p.k ? __ldg(ids + t * p.k + lane) : -1;
+    if ((unsigned)id >= (unsigned)N) id = -1;
+    float l[PER], top = -FLT_MAX;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      l[q] = q * L + lane < N ? __ldg(row + q * L + lane) : -FLT_MAX;
+      if (there(l[q])) top = fmaxf(top, fminf(l[q], FLT_MAX));
     }
+    float d = 0.f, lj = id >= 0 ? __ldg(row + id) : -FLT_MAX;
+    if (id >= 0 && grad_weights) d += __ldg(grad_weights + t * p.k + lane);
+    if (id >= 0 && grad_gates) d += __ldg(grad_gates + (int64_t)id * ld + t);
+    if (!there(lj)) id = -1;
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+    float total = 0.f;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      l[q] = there(l[q]) ? expf(fminf(l[q], FLT_MAX) - top) : 0.f;
+      total += l[q];
+    }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+    const float over = total > 0.f ? 1.f / total : 0.f;
+    const float term = id >= 0 ? p.scale * d * (expf(fminf(lj, FLT_MAX) - top) * over) : 0.f;
+    float dot = term;
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(kAll, dot, o);
+#pragma unroll
+    for (int q = 0; q < PER; ++q) l[q] *= -dot * over;
+    for (int j = 0; j < p.k; ++j) {
+      const int i = __shfl_sync(kAll, id, j, L);
+      const float x = __shfl_sync(kAll, term, j, L);
+#pragma unroll
+      for (int q = 0; q < PER; ++q)
+        if (i == q * L + lane) l[q] += x;
+    }
+    if (live)
+#pragma unroll
+      for (int q = 0; q < PER; ++q)
+        if (q * L + lane < N) grad_logits[t * N + q * L + lane] = l[q];
   }
 }
 
@@ -741,14 +958,40 @@ cudaError_t forward_threads(const RouteSpec& p, int64_t n, const float* logits, 
 }
 
 template <int K>
-cudaError_t backward_rows(const RouteSpec& p, int64_t n, const float* logits, const int32_t* ids, const float* gw,
-                          const float* gg, int64_t ld, float* out, cudaStream_t s) {
+cudaError_t backward_chosen(const RouteSpec& p, int64_t n, const float* logits, const int32_t* ids, const float* gw,
+                            const float* gg, int64_t ld, float* out, cudaStream_t s) {
   const unsigned rows = p.n <= 64 ? kRows : p.n <= 256 ? 64 : 32;  // tiles of 33 to 66 KB
-  const int64_t grid = std::min<int64_t>((n + rows - 1) / rows, kSms * 64);
-  const bool every = !p.sigmoid && !p.renormalise;
-  return launch_dependent(every ? route_backward_kernel<K, true> : route_backward_kernel<K, false>, grid, rows,
-                          sizeof(float) * rows * (every ? p.n | 1 : p.n), s, p, n, logits, ids, gw, gg, ld, out,
-                          divide_by(p.n));
+  return launch_dependent(route_chosen_backward_kernel<K>, std::min<int64_t>((n + rows - 1) / rows, kSms * 64), rows,
+                          sizeof(float) * rows * (p.n | 1), s, p, n, logits, ids, gw, gg, ld, out, divide_by(p.n));
+}
+
+template <int L, int PER>
+cudaError_t backward_every(const RouteSpec& p, int64_t n, const float* logits, const int32_t* ids, const float* gw,
+                           const float* gg, int64_t ld, float* out, cudaStream_t s) {
+  constexpr int rows = 256 / L;
+  return launch_dependent(route_every_backward_kernel<L, PER>, std::min<int64_t>((n + rows - 1) / rows, kSms * 32), 256,
+                          0, s, p, n, logits, ids, gw, gg, ld, out);
+}
+
+cudaError_t launch_backward(const RouteSpec& p, int64_t n, const float* logits, const int32_t* ids, const float* gw,
+                            const float* gg, int64_t ld, float* out, cudaStream_t s) {
+  auto run = backward_chosen<kMaxK>;
+  if (!p.sigmoid && !p.renormalise) {
+    run = p.n <= 4     ? backward_every<4, 1>
+          : p.n <= 8   ? backward_every<8, 1>
+          : p.n <= 16  ? backward_every<16, 1>
+          : p.n <= 32  ? backward_every<32, 1>
+          : p.n <= 64  ? backward_every<32, 2>
+          : p.n <= 128 ? backward_every<32, 4>
+          : p.n <= 256 ? backward_every<32, 8>
+                       : backward_every<32, 16>;
+  } else if (p.k <= 8) {
+    run = p.k == 1   ? backward_chosen<1>
+          : p.k == 2 ? backward_chosen<2>
+          : p.k <= 4 ? backward_chosen<4>
+                     : backward_chosen<8>;
+  }
+  return run(p, n, logits, ids, gw, gg, ld, out, s);
 }
 
 cudaError_t launch_forward(const RouteSpec& p, int64_t n, const float* logits, const float* bias, const RouteOut& o,
@@ -838,13 +1081,8 @@ cgtp_status cgtp_router_backward(cgtp_router router, int64_t n, const float* log
   for (const void* q : {(const void*)logits, (const void*)ids, (const void*)grad_weights, (const void*)grad_gates,
                         (const void*)grad_logits})
     if (q && !aligned16(q)) return fail(CGTP_ERR_ALIGN, "arrays must be 16-byte aligned");
-  const RouteSpec& p = router->p;
-  auto run = p.k == 1   ? backward_rows<1>
-             : p.k == 2 ? backward_rows<2>
-             : p.k <= 4 ? backward_rows<4>
-             : p.k <= 8 ? backward_rows<8>
-                        : backward_rows<kMaxK>;
-  CGTP_CUDA_TRY(run(p, n, logits, ids, grad_weights, grad_gates, ld, grad_logits, (cudaStream_t)stream));
+  CGTP_CUDA_TRY(launch_backward(router->p, n, logits, ids, grad_weights, grad_gates, ld, grad_logits,
+                                (cudaStream_t)stream));
   return CGTP_OK;
 }
 
