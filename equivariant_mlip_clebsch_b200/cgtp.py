@@ -125,20 +125,27 @@ def _args(dev, *specs):
     every argument, then a contiguous CUDA tensor on `dev`.  None passes as
     NULL (the library then reports a required argument as CGTP_ERR_NULL)."""
     types = _types()
+    at = -2 if dev is None else dev.index if dev.type == "cuda" else -2  # -2: no tensor's device
+    ptrs = []
+    for t, _, count, kind in specs:
+        if t is None:
+            ptrs.append(None)
+        elif t.dtype is types[kind] and t.numel() == count and t.get_device() == at and t.is_contiguous():
+            ptrs.append(t.data_ptr())
+        else:
+            break
+    else:
+        return ptrs
     for t, name, count, kind in specs:
         if t is not None:
             if t.dtype is not types[kind]:
                 raise TypeError(f"{name}: expected {types[kind]}, got {t.dtype}")
             if t.numel() != count:
                 raise ValueError(f"{name}: expected {count} elements, got shape {tuple(t.shape)}")
-    ptrs = []
     for t, name, _, _ in specs:
         if t is not None:
-            if not t.is_cuda or not t.is_contiguous() or (dev is not None and t.device != dev):
-                _require_device(t, name, dev)
-            t = t.data_ptr()
-        ptrs.append(t)
-    return ptrs
+            _require_device(t, name, dev)
+    return [None if t is None else t.data_ptr() for t, _, _, _ in specs]
 
 
 def _workspace(t, dev):
@@ -534,7 +541,7 @@ class LayerNorm:
 
     def _like(self, x, n):
         """A new [n, D] array for x (empty_like is the cheaper call)."""
-        if x.dim() == 2 and x.dtype is _types()["f32"] and x.is_contiguous() and x.shape[1] == self.d:
+        if x.dtype is _types()["f32"] and x.dim() == 2 and x.shape[1] == self.d:
             return _torch().empty_like(x)
         return self._new(x, n, self.d)
 

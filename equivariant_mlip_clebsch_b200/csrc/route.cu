@@ -37,8 +37,18 @@ __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// 1 / (1 + e^-l); CUDA's fast exponential and division
-__device__ __forceinline__ float quick_sigmoid(float l) { return __fdividef(1.f, 1.f + __expf(-l)); }
+// The hardware's 2^x and 1 / x (2 ulp and 1 ulp), subnormals as zero: without
+// the steps around them that keep subnormals.
+__device__ __forceinline__ float quick_exp(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+__device__ __forceinline__ float quick_sigmoid(float l) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + quick_exp(-l)));
+  return y;
+}
 
 template <class X>
 __device__ __forceinline__ X warp_sum(X v) {
@@ -187,8 +197,8 @@ __device__ __forceinline__ int ordered(float v) {  // an integer in the order of
 __device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
 
 // The error of a compared value.
-//   sigmoid: 1 / (1 + __expf(-l)): the exponent's rounding and the function's error
-//   give s (1 - s) (|l| 2^-24 + 2^-22) < 8e-8, the division 2 ulp: |ds| < 2e-7
+//   sigmoid: 1 / (1 + 2^(-l log2 e)): the exponent's two roundings and the function's error
+//   give s (1 - s) (|l| 2^-23 + 2^-22) < 1e-7, the reciprocal 1 ulp: |ds| < 2e-7
 //   softmax: exp(l - top) off by < 2.7e-7 in the same way; the sum's relative
 //   error, in eight partial sums at least, (n / 8 + 4) 2^-24, is common to all
 //   scores <= 1
@@ -218,7 +228,7 @@ __device__ __forceinline__ bool route_row_fast(const RouteSpec& p, const float* 
   float s[PER], total = 0.f;
 #pragma unroll
   for (int q = 0; q < PER; ++q) {
-    s[q] = !there(l[q]) ? 0.f : p.sigmoid ? quick_sigmoid(l[q]) : __expf(l[q] - top);
+    s[q] = !there(l[q]) ? 0.f : p.sigmoid ? quick_sigmoid(l[q]) : quick_exp(l[q] - top);
     total += s[q];
   }
   float over = 1.f;
@@ -415,12 +425,13 @@ __global__ void __launch_bounds__(2 * kRows) route_thread_kernel(
     int32_t* __restrict__ counts, unsigned magic) {
   grid_dependency_wait();
   grid_launch_dependents();
-  extern __shared__ float smem[];
+  extern __shared__ float4 smem4[];
+  float* smem = reinterpret_cast<float*>(smem4);
   constexpr int S = kRows + 1;  // odd: neither filling nor reading meets one bank
   const int tid = threadIdx.x & (kRows - 1), half = threadIdx.x / kRows, lane = tid & 31, N = p.n;
-  float* tile = smem;                                  // [N][S]
-  float* sb = tile + N * S;                            // [N] bias
-  int* hist = reinterpret_cast<int*>(sb + N);          // [N]
+  float* sb = smem;                                    // [N] bias, in whole float4s
+  float* tile = sb + (N + 3) / 4 * 4;                  // [N][S]
+  int* hist = reinterpret_cast<int*>(tile + N * S);    // [N]
   unsigned* skept = reinterpret_cast<unsigned*>(hist + N);  // [kRows] groups kept
   float* swap = reinterpret_cast<float*>(skept + kRows);    // [swap_rows][kRows], what the halves tell one another
   for (int e = threadIdx.x; e < N; e += 2 * kRows) {
@@ -433,11 +444,13 @@ __global__ void __launch_bounds__(2 * kRows) route_thread_kernel(
   const float base = value_error(N, SIGMOID);
   const int size = N / p.groups, split = (size + 1) / 2;
   const int from = half ? split : 0, to = half ? size : split;  // this thread's part of a group
+  const bool fours = size % 8 == 0;                             // both parts are whole fours
   for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < n; t0 += (int64_t)gridDim.x * kRows) {
     const int rows = (int)min((int64_t)kRows, n - t0);
     __syncthreads();  // the tile of the round before is read
     const float* src = logits + t0 * N;  // rows N values from a 16-byte border
     if (N % 4 == 0) {
+#pragma unroll 8
       for (int i = threadIdx.x * 4; i < rows * N; i += 8 * kRows) {
         const float4 f = __ldg(reinterpret_cast<const float4*>(src + i));
         const int r = (int)__umulhi(i, magic);
@@ -448,6 +461,7 @@ __global__ void __launch_bounds__(2 * kRows) route_thread_kernel(
         dst[3 * S] = f.w;
       }
     } else {
+#pragma unroll 8
       for (int i = threadIdx.x; i < rows * N; i += 2 * kRows) {
         const int r = N == 1 ? i : (int)__umulhi(i, magic);
         tile[(i - r * N) * S + r] = __ldg(src + i);
@@ -472,7 +486,7 @@ __global__ void __launch_bounds__(2 * kRows) route_thread_kernel(
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float l = e + j < e1 ? col[(e + j) * S] : -FLT_MAX;
-          part[j] += there(l) ? __expf(fminf(l, FLT_MAX) - top) : 0.f;
+          part[j] += there(l) ? quick_exp(fminf(l, FLT_MAX) - top) : 0.f;
         }
       total = (part[0] + part[1]) + (part[2] + part[3]);
       __syncthreads();
@@ -484,7 +498,7 @@ __global__ void __launch_bounds__(2 * kRows) route_thread_kernel(
     const float over = total > 0.f ? 1.f / total : 0.f;
     auto value = [&](float l, float b) {  // what is compared; -inf where the expert is out
       if (BY_LOGIT) return there(l) ? fminf(l, FLT_MAX) : -INFINITY;
-      const float s = SIGMOID ? quick_sigmoid(l) : __expf(fminf(l, FLT_MAX) - top) * over;
+      const float s = SIGMOID ? quick_sigmoid(l) : quick_exp(fminf(l, FLT_MAX) - top) * over;
       return there(l) ? s + b : -INFINITY;
     };
     const float wide = 2.f * base;  // bound on the error of a difference of two values, with 2^-23 of each
@@ -512,14 +526,25 @@ __global__ void __launch_bounds__(2 * kRows) route_thread_kernel(
       // the best two of every group, of each half
       for (int g = 0; g < p.groups; ++g) {
         float b1 = -INFINITY, b2 = -INFINITY;
-        float* c = col + g * size * S;
-        const float* b = sb + g * size;
-#pragma unroll 4
-        for (int i = from; i < to; ++i) {
-          const float v = value(c[i * S], b[i]);
-          c[i * S] = v;  // from here on the tile holds the values
+        float* c = col + (g * size + from) * S;
+        const float* b = sb + g * size + from;
+        auto look = [&](float* at, float bi) {
+          const float v = value(*at, bi);
+          *at = v;  // from here on the tile holds the values
           b2 = fmaxf(b2, fminf(b1, v));
           b1 = fmaxf(b1, v);
+        };
+        if (fours) {
+          for (int i = from; i < to; i += 4, c += 4 * S, b += 4) {
+            const float4 bi = *reinterpret_cast<const float4*>(b);
+            look(c, bi.x);
+            look(c + S, bi.y);
+            look(c + 2 * S, bi.z);
+            look(c + 3 * S, bi.w);
+          }
+        } else {
+#pragma unroll 1
+          for (int i = from; i < to; ++i, c += S, ++b) look(c, *b);
         }
         float* at = swap + 2 * g * kRows + tid;
         if (half) {
@@ -568,14 +593,30 @@ __global__ void __launch_bounds__(2 * kRows) route_thread_kernel(
       __syncthreads();
       kept = skept[tid];
       for (unsigned left = kept; left; left &= left - 1) {
-        const int e0 = (__ffs(left) - 1) * size;
-        const float* c = col + e0 * S;
-#pragma unroll 4
-        for (int i = from; i < to; ++i) insert(key_of(c[i * S], e0 + i, mask));
+        int e = (__ffs(left) - 1) * size + from;
+        const int end = e + to - from;
+        const float* c = col + e * S;
+        if (fours) {
+          for (; e < end; e += 4, c += 4 * S) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) insert(key_of(c[j * S], e + j, mask));
+          }
+        } else {
+#pragma unroll 1
+          for (; e < end; ++e, c += S) insert(key_of(*c, e, mask));
+        }
       }
     } else {
-#pragma unroll 4
-      for (int e = from; e < to; ++e) insert(key_of(value(col[e * S], sb[e]), e, mask));
+      const float* c = col + from * S;
+      if (fours) {
+        for (int e = from; e < to; e += 4, c += 4 * S) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) insert(key_of(value(c[j * S], sb[e + j]), e + j, mask));
+        }
+      } else {
+#pragma unroll 1
+        for (int e = from; e < to; ++e, c += S) insert(key_of(value(*c, sb[e]), e, mask));
+      }
       if (half && gates) clear_gates();
     }
     if (half) {
@@ -658,7 +699,8 @@ __global__ void __launch_bounds__(2 * kRows) route_thread_kernel(
 #pragma unroll
         for (int j = 0; j < K; ++j)
           if (idx[j] >= 0)
-            w[j] = w[j] > 0.f || !p.renormalise ? 1.f / (1.f + expf(-w[j])) : expf(w[j] - m) / (1.f + expf(w[j]));
+            w[j] = w[j] > 0.f || !p.renormalise ? __fdividef(1.f, 1.f + expf(-w[j]))
+                                                : __fdividef(expf(w[j] - m), 1.f + expf(w[j]));
       } else {
         m = p.renormalise ? m : top;
 #pragma unroll
@@ -948,7 +990,7 @@ template <int K>
 cudaError_t forward_threads(const RouteSpec& p, int64_t n, const float* logits, const float* bias, const RouteOut& o,
                             cudaStream_t s) {
   const int swap_rows = std::max(K + 1, p.groups > 1 ? 4 * p.groups : 2);
-  const size_t shared = sizeof(float) * ((size_t)(kRows + 1) * p.n + 2 * p.n + (size_t)(1 + swap_rows) * kRows);
+  const size_t shared = sizeof(float) * ((size_t)(kRows + 1) * p.n + 2 * p.n + 4 + (size_t)(1 + swap_rows) * kRows);
   const int64_t grid = std::min<int64_t>((n + kRows - 1) / kRows, kSms * 64);
   auto kernel = !bias && p.groups == 1 ? route_thread_kernel<K, false, true>
                 : p.sigmoid            ? route_thread_kernel<K, true, false>
