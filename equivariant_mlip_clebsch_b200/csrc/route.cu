@@ -57,144 +57,136 @@ __device__ __forceinline__ X warp_sum(X v) {
   return v;
 }
 
-// The best (largest value, lowest index) of the warp's pairs.
-__device__ __forceinline__ void warp_best(double& v, int& i) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const double w = __shfl_xor_sync(kAll, v, o);
-    const int j = __shfl_xor_sync(kAll, i, o);
-    if (w > v || (w == v && j < i)) {
-      v = w;
-      i = j;
-    }
-  }
-}
-
 __device__ __forceinline__ bool there(float l) { return l > -FLT_MAX; }
-
-// One row by one warp with every compared value in 64 bits; lane i holds the
-// experts i, i + 32, ... (PER of them).  Lane j returns the j-th choice and
-// its weight (-1 and 0 where nothing is left).
-template <int PER>
-__device__ __forceinline__ void route_row(const RouteSpec& p, const float* row, const float* bias, int* id_out,
-                                          float* w_out) {
-  const int lane = threadIdx.x & 31, size = p.n / p.groups;
-  double s[PER], v[PER];
-  float top = -FLT_MAX;
-  unsigned on = 0;
-#pragma unroll
-  for (int q = 0; q < PER; ++q) {
-    const int e = q * 32 + lane;
-    const float l = e < p.n ? row[e] : -FLT_MAX;
-    if (there(l)) {
-      on |= 1u << q;
-      top = fmaxf(top, fminf(l, FLT_MAX));
-    }
-    s[q] = (double)fminf(l, FLT_MAX);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-  double total = 0.0;
-#pragma unroll
-  for (int q = 0; q < PER; ++q) {
-    s[q] = !(on >> q & 1) ? 0.0 : p.sigmoid ? 1.0 / (1.0 + exp(-s[q])) : exp(s[q] - (double)top);
-    total += s[q];
-  }
-  if (!p.sigmoid) {
-    total = warp_sum(total);
-#pragma unroll
-    for (int q = 0; q < PER; ++q) s[q] = total > 0.0 ? s[q] / total : 0.0;
-  }
-#pragma unroll
-  for (int q = 0; q < PER; ++q) {
-    v[q] = -INFINITY;
-    if (on >> q & 1) {
-      // without bias and groups the logits' own order, which the scores lose where they saturate
-      v[q] = bias ? s[q] + (double)bias[q * 32 + lane]
-             : p.groups > 1 ? s[q]
-                            : (double)fminf(row[q * 32 + lane], FLT_MAX);
-      if (!(v[q] > -INFINITY)) v[q] = -INFINITY;
-    }
-  }
-  if (p.groups > 1) {
-    double mine = -INFINITY;  // lane g: the score of group g
-    for (int g = 0; g < p.groups; ++g) {
-      double sum = -INFINITY;
-      int taken = -1;
-      for (int r = 0; r < p.group_best; ++r) {
-        double b = -INFINITY;
-        int at = kMaxExperts;
-#pragma unroll
-        for (int q = 0; q < PER; ++q) {
-          const int e = q * 32 + lane;
-          if (e >= g * size && e < (g + 1) * size && e != taken && v[q] > b) {
-            b = v[q];
-            at = e;
-          }
-        }
-        warp_best(b, at);
-        if (b > -INFINITY) sum = r == 0 ? b : sum + b;
-        taken = at;
-      }
-      if (lane == g) mine = sum;
-    }
-    unsigned kept = 0;
-    for (int r = 0; r < p.top_groups; ++r) {
-      double b = lane < p.groups && !(kept >> lane & 1) ? mine : -INFINITY;
-      int at = b > -INFINITY ? lane : 64;
-      warp_best(b, at);
-      if (at < 32) kept |= 1u << at;
-    }
-#pragma unroll
-    for (int q = 0; q < PER; ++q) {
-      const int e = q * 32 + lane;
-      if (e < p.n && !(kept >> (e / size) & 1)) v[q] = -INFINITY;
-    }
-  }
-  int id = -1;
-  for (int j = 0; j < p.k; ++j) {
-    double b = -INFINITY;
-    int at = kMaxExperts;
-#pragma unroll
-    for (int q = 0; q < PER; ++q)
-      if (v[q] > b) {
-        b = v[q];
-        at = q * 32 + lane;
-      }
-    warp_best(b, at);
-#pragma unroll
-    for (int q = 0; q < PER; ++q)
-      if (q * 32 + lane == at) v[q] = -INFINITY;
-    if (lane == j && at < kMaxExperts) id = at;
-  }
-  // The weights.  Renormalised ones relative to the largest chosen logit (for
-  // the sigmoid where that is negative): the chosen scores may all lie below
-  // the smallest float.
-  const double l = id >= 0 ? (double)fminf(row[id], FLT_MAX) : 0.0;
-  double w = 0.0;
-  if (!p.renormalise) {
-    if (id >= 0) w = p.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top) / total;
-  } else {
-    double m = id >= 0 ? l : -INFINITY;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(kAll, m, o));
-    if (p.sigmoid) m = fmin(m, 0.0);
-    if (id >= 0) w = !p.sigmoid ? exp(l - m) : l <= 0.0 ? exp(l - m) / (1.0 + exp(l)) : 1.0 / (1.0 + exp(-l));
-    const double sum = warp_sum(w);
-    if (id >= 0) w /= sum;
-  }
-  *id_out = id;
-  *w_out = (float)((double)p.scale * w);
-}
-
-// ---- one row by one warp in FP32: false where two compared values are closer
-// than their error (then route_row decides)
 
 __device__ __forceinline__ int ordered(float v) {  // an integer in the order of the values
   const int i = __float_as_int(v);
   return i ^ ((i >> 31) & 0x7fffffff);
 }
 __device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+
+// One row by one warp with every compared value in 64 bits, v [n] in shared
+// memory of the warp's own.  Lane j returns the j-th choice and its weight (-1 and
+// 0 where nothing is left).
+//
+// It runs for few rows, each at the end of a CTA that others wait for, and what
+// it costs there is the fetch of its instructions: so it is one function of loops
+// that are not unrolled (inlined and unrolled, the 60 such rows of 172,050 took 16
+// of the 68 us of the whole forward).
+__device__ __noinline__ double exp_64(double x) { return exp(x); }
+
+__device__ __noinline__ void route_row(const RouteSpec* spec, const float* row, const float* bias, double* v,
+                                       int* id_out, float* w_out) {
+  const RouteSpec p = *spec;
+  const int lane = threadIdx.x & 31, size = p.n / p.groups;
+  int most = INT_MIN;
+#pragma unroll 1
+  for (int e = lane; e < p.n; e += 32)
+    if (there(row[e])) most = max(most, ordered(fminf(row[e], FLT_MAX)));
+  most = __reduce_max_sync(kAll, most);
+  const double top = most == INT_MIN ? 0.0 : (double)unordered(most);
+  double total = 0.0;
+#pragma unroll 1
+  for (int e = lane; e < p.n; e += 32) {
+    const double l = (double)fminf(row[e], FLT_MAX), x = exp_64(p.sigmoid ? -l : l - top);
+    const double s = !there(row[e]) ? -1.0 : p.sigmoid ? 1.0 / (1.0 + x) : x;
+    v[e] = s;
+    if (s >= 0.0) total += s;
+  }
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+#pragma unroll 1
+  for (int e = lane; e < p.n; e += 32) {
+    double x = v[e];
+    if (x < 0.0) {
+      x = -INFINITY;
+    } else if (!bias && p.groups == 1) {
+      x = (double)fminf(row[e], FLT_MAX);  // the scores' order, which they lose where they saturate
+    } else {
+      x = (p.sigmoid ? x : x / total) + (bias ? (double)bias[e] : 0.0);
+      if (!(x > -INFINITY)) x = -INFINITY;
+    }
+    v[e] = x;
+  }
+  __syncwarp();
+  // the warp's best pair: the largest value, of equal ones the lowest index
+  auto meet = [&](double& b, int& at) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const double w = __shfl_xor_sync(kAll, b, o);
+      const int j = __shfl_xor_sync(kAll, at, o);
+      if (w > b || (w == b && j < at)) {
+        b = w;
+        at = j;
+      }
+    }
+  };
+  if (p.groups > 1) {  // lane g scores group g; a group's rank is the number of better ones
+    double b1 = -INFINITY, b2 = -INFINITY;
+    if (lane < p.groups)
+#pragma unroll 4
+      for (int i = 0; i < size; ++i) {
+        const double x = v[lane * size + i];
+        b2 = x > b1 ? b1 : x > b2 ? x : b2;
+        b1 = x > b1 ? x : b1;
+      }
+    const double score = p.group_best == 2 && b2 > -INFINITY ? b1 + b2 : b1;
+    int rank = 0;
+#pragma unroll 4
+    for (int g = 0; g < p.groups; ++g) {
+      const double other = __shfl_sync(kAll, score, g);
+      rank += other > score || (other == score && g < lane);
+    }
+    const unsigned kept = __ballot_sync(kAll, lane < p.groups && rank < p.top_groups);
+#pragma unroll 1
+    for (int e = lane; e < p.n; e += 32)
+      if (!(kept >> (e / size) & 1)) v[e] = -INFINITY;
+    __syncwarp();
+  }
+  int id = -1;
+#pragma unroll 1
+  for (int j = 0; j < p.k; ++j) {
+    double b = -INFINITY;
+    int at = kMaxExperts;
+#pragma unroll 1
+    for (int e = lane; e < p.n; e += 32)
+      if (v[e] > b) {
+        b = v[e];
+        at = e;
+      }
+    meet(b, at);
+    if (at == kMaxExperts) break;
+    if (lane == j) id = at;
+    __syncwarp();
+    if (lane == 0) v[at] = -INFINITY;
+    __syncwarp();
+  }
+  // The weights.  Renormalised ones relative to the largest chosen logit (for
+  // the sigmoid where that is negative): the chosen scores may all lie below
+  // the smallest float.
+  const double l = id >= 0 ? (double)fminf(row[id], FLT_MAX) : 0.0;
+  double m = top;
+  if (p.renormalise) {
+    m = (double)unordered(__reduce_max_sync(kAll, id >= 0 ? ordered((float)l) : ordered(-FLT_MAX)));
+    if (p.sigmoid) m = fmin(m, 0.0);
+  } else if (p.sigmoid) {
+    m = 0.0;
+  }
+  // softmax e^(l - m); sigmoid e^(l - m) / (1 + e^l), for positive l (m = 0) 1 / (1 + e^-l)
+  const double x = exp_64(p.sigmoid ? -fabs(l) : l - m);
+  double w = p.sigmoid ? (l > 0.0 ? 1.0 : exp_64(l - m)) / (1.0 + x) : x;
+  if (id < 0) w = 0.0;
+  double sum = w;
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+  if (!p.renormalise) sum = p.sigmoid ? 1.0 : total;
+  *id_out = id;
+  *w_out = id < 0 ? 0.f : (float)((double)p.scale * (w / sum));
+  __syncwarp();
+}
+
+// ---- one row by one warp in FP32: false where two compared values are closer
+// than their error (then route_row decides)
 
 // The error of a compared value.
 //   sigmoid: 1 / (1 + 2^(-l log2 e)): the exponent's two roundings and the function's error
@@ -206,6 +198,22 @@ __device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((
 // A difference of two is off by twice that; a group's score adds two values.
 __device__ __forceinline__ float value_error(int n, bool sigmoid) {
   return sigmoid ? 4e-7f : 6e-7f + (float)(n / 8 + 4) * 6e-8f;
+}
+
+// The weight of a warp's row: lane j has the j-th choice (-1: none) and its
+// logit; the row's largest logit and one over its softmax's sum.
+__device__ __forceinline__ float row_weight(const RouteSpec& p, int id, float l, float top, float over) {
+  float w = 0.f;
+  if (!p.renormalise) {
+    if (id >= 0) w = p.sigmoid ? 1.f / (1.f + expf(-l)) : expf(l - top) * over;
+  } else {  // relative to the largest: see route_row
+    float m = unordered(__reduce_max_sync(kAll, id >= 0 ? ordered(l) : INT_MIN));
+    if (p.sigmoid) m = fminf(m, 0.f);
+    if (id >= 0) w = !p.sigmoid ? expf(l - m) : l > 0.f ? 1.f / (1.f + expf(-l)) : expf(l - m) / (1.f + expf(l));
+    const float sum = warp_sum(w);
+    if (id >= 0) w /= sum;
+  }
+  return p.scale * w;
 }
 
 template <int PER>
@@ -329,40 +337,31 @@ __device__ __forceinline__ bool route_row_fast(const RouteSpec& p, const float* 
     if (!same(before, at)) return false;
     drop(at);
   }
-  // weights, as in route_row
-  const float lj = id >= 0 ? fminf(__ldg(row + max(id, 0)), FLT_MAX) : 0.f;
-  float w = 0.f;
-  if (!p.renormalise) {
-    if (id >= 0) w = p.sigmoid ? 1.f / (1.f + expf(-lj)) : expf(lj - top) * over;
-  } else {
-    float m = unordered(__reduce_max_sync(kAll, id >= 0 ? ordered(lj) : kLow));
-    if (p.sigmoid) m = fminf(m, 0.f);
-    if (id >= 0) w = !p.sigmoid ? expf(lj - m) : lj > 0.f ? 1.f / (1.f + expf(-lj)) : expf(lj - m) / (1.f + expf(lj));
-    const float sum = warp_sum(w);
-    if (id >= 0) w /= sum;
-  }
   *id_out = id;
-  *w_out = p.scale * w;
+  *w_out = row_weight(p, id, id >= 0 ? fminf(__ldg(row + max(id, 0)), FLT_MAX) : 0.f, top, over);
   return true;
 }
 
 // ---- forward, one warp a row, eight rows a CTA (few rows, many experts, k > 8)
 
 template <int PER>
-__global__ void __launch_bounds__(256) route_warp_kernel(RouteSpec p, int64_t n, const float* __restrict__ logits,
+__global__ void __launch_bounds__(256) route_warp_kernel(const __grid_constant__ RouteSpec p, int64_t n, const float* __restrict__ logits,
                                                          const float* __restrict__ bias, int32_t* __restrict__ ids,
                                                          float* __restrict__ weights, float* __restrict__ gates,
                                                          int64_t ld, int32_t* __restrict__ counts) {
   grid_dependency_wait();
   grid_launch_dependents();
-  __shared__ float tile[PER * 32 * 9];  // gates of eight rows, [expert][9]
+  constexpr int S = PER < 16 ? 9 : 8;  // 48 KB in all at 512 experts
+  __shared__ float tile[PER * 32 * S];  // gates of eight rows, [expert][S]
+  __shared__ double exact[8][PER * 32];
   const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
   for (int64_t t0 = (int64_t)blockIdx.x * 8; t0 < n; t0 += (int64_t)gridDim.x * 8) {
     const int64_t t = t0 + r;
     if (t < n) {  // whole warps
       int id;
       float w;
-      if (!route_row_fast<PER>(p, logits + t * p.n, bias, &id, &w)) route_row<PER>(p, logits + t * p.n, bias, &id, &w);
+      if (!route_row_fast<PER>(p, logits + t * p.n, bias, &id, &w))
+        route_row(&p, logits + t * p.n, bias, exact[r], &id, &w);
       if (lane < p.k) {
         if (ids) ids[t * p.k + lane] = id;
         if (weights) weights[t * p.k + lane] = w;
@@ -370,15 +369,15 @@ __global__ void __launch_bounds__(256) route_warp_kernel(RouteSpec p, int64_t n,
       }
       if (gates) {
 #pragma unroll
-        for (int q = 0; q < PER; ++q) tile[(q * 32 + lane) * 9 + r] = 0.f;
+        for (int q = 0; q < PER; ++q) tile[(q * 32 + lane) * S + r] = 0.f;
         __syncwarp();
-        if (id >= 0) tile[id * 9 + r] = w;
+        if (id >= 0) tile[id * S + r] = w;
       }
     }
     if (gates) {
       __syncthreads();
       for (int i = threadIdx.x; i < p.n * 8; i += 256)
-        if (t0 + (i & 7) < n) gates[(int64_t)(i >> 3) * ld + t0 + (i & 7)] = tile[(i >> 3) * 9 + (i & 7)];
+        if (t0 + (i & 7) < n) gates[(int64_t)(i >> 3) * ld + t0 + (i & 7)] = tile[(i >> 3) * S + (i & 7)];
       __syncthreads();
     }
   }
@@ -410,7 +409,7 @@ __device__ __forceinline__ float key_top(int key, int mask) {
 // most twice value_error against one another; where a decision is closer than that
 // the row is looked at again (two experts of equal logit and bias are in their
 // right order already) and, if that does not settle it, decided in 64 bits by the
-// whole warp.  The k + 1 best are found as integer keys (two instructions a
+// whole warp: the few experts that may be among the k best, one a lane.  The k + 1 best are found as integer keys (two instructions a
 // place and expert) that hold the index in their
 // low bits; the keys' order is put right from the values themselves.
 //
@@ -419,8 +418,8 @@ __device__ __forceinline__ float key_top(int key, int mask) {
 // by experts, [expert][row], so that a thread's experts are constant offsets from
 // one address.
 template <int K, bool SIGMOID, bool BY_LOGIT>
-__global__ void __launch_bounds__(2 * kRows) route_thread_kernel(
-    RouteSpec p, int64_t n, const float* __restrict__ logits, const float* __restrict__ bias,
+__global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
+    const __grid_constant__ RouteSpec p, int64_t n, const float* __restrict__ logits, const float* __restrict__ bias,
     int32_t* __restrict__ ids, float* __restrict__ weights, float* __restrict__ gates, int64_t ld,
     int32_t* __restrict__ counts, unsigned magic) {
   grid_dependency_wait();
@@ -429,11 +428,12 @@ __global__ void __launch_bounds__(2 * kRows) route_thread_kernel(
   float* smem = reinterpret_cast<float*>(smem4);
   constexpr int S = kRows + 1;  // odd: neither filling nor reading meets one bank
   const int tid = threadIdx.x & (kRows - 1), half = threadIdx.x / kRows, lane = tid & 31, N = p.n;
-  float* sb = smem;                                    // [N] bias, in whole float4s
+  double* exact = reinterpret_cast<double*>(smem4);    // [4][N] of the warps that decide
+  float* sb = smem + 8 * N;                            // [N] bias, in whole float4s
   float* tile = sb + (N + 3) / 4 * 4;                  // [N][S]
   int* hist = reinterpret_cast<int*>(tile + N * S);    // [N]
-  unsigned* skept = reinterpret_cast<unsigned*>(hist + N);  // [kRows] groups kept
-  float* swap = reinterpret_cast<float*>(skept + kRows);    // [swap_rows][kRows], what the halves tell one another
+  unsigned* skept = reinterpret_cast<unsigned*>(hist + N);  // [kRows] groups kept, then [4][kRows] experts chosen
+  float* swap = reinterpret_cast<float*>(skept + 4 * kRows);  // [swap_rows][kRows], what the halves tell one another
   for (int e = threadIdx.x; e < N; e += 2 * kRows) {
     const float b = bias ? __ldg(bias + e) : 0.f;
     sb[e] = b >= -INFINITY ? b : -INFINITY;  // a NaN rules the expert out too
@@ -496,14 +496,19 @@ __global__ void __launch_bounds__(2 * kRows) route_thread_kernel(
       __syncthreads();
     }
     const float over = total > 0.f ? 1.f / total : 0.f;
-    auto value = [&](float l, float b) {  // what is compared; -inf where the expert is out
-      if (BY_LOGIT) return there(l) ? fminf(l, FLT_MAX) : -INFINITY;
+    auto score = [&](float l) {  // -1 where the expert is out
       const float s = SIGMOID ? quick_sigmoid(l) : quick_exp(fminf(l, FLT_MAX) - top) * over;
-      return there(l) ? s + b : -INFINITY;
+      return there(l) ? s : -1.f;
+    };
+    auto biased = [&](float s, float b) { return s < 0.f ? -INFINITY : s + b; };
+    // what is compared, from the tile: logits, with groups (once they are scored) scores
+    auto value = [&](float x, float b) {
+      if (BY_LOGIT) return there(x) ? fminf(x, FLT_MAX) : -INFINITY;
+      return biased(p.groups > 1 ? x : score(x), b);
     };
     const float wide = 2.f * base;  // bound on the error of a difference of two values, with 2^-23 of each
     auto apart = [&](float a, float b) { return BY_LOGIT ? a > b : a - b > wide + 1.2e-7f * (fabsf(a) + fabsf(b)); };
-    bool doubt = false;
+    bool doubt = false, hard = false;  // hard: 64 bits from the start
     unsigned kept = 1;
     int key[K + 1];
 #pragma unroll
@@ -516,12 +521,6 @@ __global__ void __launch_bounds__(2 * kRows) route_thread_kernel(
         key[j] = a;
       }
     };
-    auto clear_gates = [&]() {  // a warp writes 32 rows of one expert
-      float* out = gates + t0;
-      if (live)
-#pragma unroll 4
-        for (int e = 0; e < N; ++e, out += ld) out[tid] = 0.f;
-    };
     if (p.groups > 1) {
       // the best two of every group, of each half
       for (int g = 0; g < p.groups; ++g) {
@@ -529,8 +528,8 @@ __global__ void __launch_bounds__(2 * kRows) route_thread_kernel(
         float* c = col + (g * size + from) * S;
         const float* b = sb + g * size + from;
         auto look = [&](float* at, float bi) {
-          const float v = value(*at, bi);
-          *at = v;  // from here on the tile holds the values
+          const float s = score(*at), v = biased(s, bi);
+          *at = s;  // from here on the tile holds the scores
           b2 = fmaxf(b2, fminf(b1, v));
           b1 = fmaxf(b1, v);
         };
@@ -556,9 +555,7 @@ __global__ void __launch_bounds__(2 * kRows) route_thread_kernel(
         }
       }
       __syncthreads();
-      if (half) {
-        if (gates) clear_gates();
-      } else {
+      if (!half) {
         for (int g = 0; g < p.groups; ++g) {
           float* at = swap + 2 * g * kRows + tid;
           const float a1 = at[0], a2 = at[kRows], c1 = at[2 * p.groups * kRows], c2 = at[(2 * p.groups + 1) * kRows];
@@ -587,7 +584,7 @@ __global__ void __launch_bounds__(2 * kRows) route_thread_kernel(
         float next = -INFINITY;
 #pragma unroll 4
         for (int g = 0; g < p.groups; ++g) next = fmaxf(next, swap[2 * g * kRows + tid]);
-        doubt = next > -INFINITY && !(last - next > 2.f * wide + 2.4e-7f * (fabsf(last) + fabsf(next)));
+        hard = next > -INFINITY && !(last - next > 2.f * wide + 2.4e-7f * (fabsf(last) + fabsf(next)));
         skept[tid] = kept;
       }
       __syncthreads();
@@ -599,11 +596,11 @@ __global__ void __launch_bounds__(2 * kRows) route_thread_kernel(
         if (fours) {
           for (; e < end; e += 4, c += 4 * S) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) insert(key_of(c[j * S], e + j, mask));
+            for (int j = 0; j < 4; ++j) insert(key_of(value(c[j * S], sb[e + j]), e + j, mask));
           }
         } else {
 #pragma unroll 1
-          for (; e < end; ++e, c += S) insert(key_of(*c, e, mask));
+          for (; e < end; ++e, c += S) insert(key_of(value(*c, sb[e]), e, mask));
         }
       }
     } else {
@@ -617,105 +614,105 @@ __global__ void __launch_bounds__(2 * kRows) route_thread_kernel(
 #pragma unroll 1
         for (int e = from; e < to; ++e, c += S) insert(key_of(value(*c, sb[e]), e, mask));
       }
-      if (half && gates) clear_gates();
     }
     if (half) {
 #pragma unroll
       for (int j = 0; j <= K; ++j) swap[j * kRows + tid] = __int_as_float(key[j]);
     }
     __syncthreads();
-    if (half) continue;  // the next round's first barrier waits for the other half
+    if (!half) {
 #pragma unroll
-    for (int j = 0; j <= K; ++j) insert(__float_as_int(swap[j * kRows + tid]));
-    // the value behind a key, as it was compared
-    auto held = [&](int k, int& e) {
-      e = mask - (k & mask);
-      const bool some = k != INT_MIN;
-      if (!some) e = 0;
-      const float v = p.groups > 1 ? col[e * S] : value(col[e * S], sb[e]);
-      return some ? v : -INFINITY;
-    };
-    float val[K + 1];
-    int idx[K + 1];
+      for (int j = 0; j <= K; ++j) insert(__float_as_int(swap[j * kRows + tid]));
+      // the values behind the keys, as they were compared
+      float val[K + 1];
+      int idx[K + 1];
 #pragma unroll
-    for (int j = 0; j <= K; ++j) val[j] = held(key[j], idx[j]);
-    const float outside = key[K] != INT_MIN ? key_top(key[K], mask) : -INFINITY;  // no smaller key has more
+      for (int j = 0; j <= K; ++j) {
+        const bool some = key[j] != INT_MIN;
+        idx[j] = some ? mask - (key[j] & mask) : 0;
+        const float v = value(col[idx[j] * S], sb[idx[j]]);
+        val[j] = some ? v : -INFINITY;
+      }
+      const float outside = key[K] != INT_MIN ? key_top(key[K], mask) : -INFINITY;  // no smaller key has more
 #pragma unroll
-    for (int j = K; j > 0; --j)  // neighbours that the keys' cut bits put the wrong way round
-      if (val[j] > val[j - 1]) {
+      for (int j = K; j > 0; --j) {  // neighbours that the keys' cut bits put the wrong way round
+        const bool wrong = val[j] > val[j - 1];
         const float a = val[j];
-        val[j] = val[j - 1];
-        val[j - 1] = a;
+        val[j] = wrong ? val[j - 1] : a;
+        val[j - 1] = wrong ? a : val[j - 1];
         const int b = idx[j];
-        idx[j] = idx[j - 1];
-        idx[j - 1] = b;
+        idx[j] = wrong ? idx[j - 1] : b;
+        idx[j - 1] = wrong ? b : idx[j - 1];
       }
-    bool close = false;
-    float lastv = -INFINITY;
-    int lastid = -1;
+      bool close = false;
+      float lastv = -INFINITY;
+      int lastid = -1;
 #pragma unroll
-    for (int j = 0; j < K; ++j)
-      if (j < p.k && val[j] > -INFINITY) {
-        close |= val[j + 1] > -INFINITY && !apart(val[j], val[j + 1]);
-        lastv = val[j];
-        lastid = idx[j];
+      for (int j = 0; j < K; ++j) {
+        const bool in = j < p.k && val[j] > -INFINITY;
+        close |= in && val[j + 1] > -INFINITY && !apart(val[j], val[j + 1]);
+        lastv = in ? val[j] : lastv;
+        lastid = in ? idx[j] : lastid;
       }
-    // Experts behind the last key: at most `outside`.  (Where fewer than k are
-    // left, the list holds them all and what is behind is -inf.)
-    close |= lastid >= 0 && outside > -INFINITY && val[K] > -INFINITY && !apart(lastv, outside);
-    if (close && !doubt) {
+      // Experts behind the last key: at most `outside`.  (Where fewer than k are
+      // left, the list holds them all and what is behind is -inf.)
+      close |= lastid >= 0 && outside > -INFINITY && val[K] > -INFINITY && !apart(lastv, outside);
+      if (close && live && !hard) {
+        auto same = [&](int a, int b) { return a < b && __ldg(row + a) == __ldg(row + b) && sb[a] == sb[b]; };
 #pragma unroll
-      for (int j = 0; j + 1 < K; ++j)
-        if (j + 1 < p.k && val[j + 1] > -INFINITY && !apart(val[j], val[j + 1]))
-          doubt |= !(__ldg(row + idx[j]) == __ldg(row + idx[j + 1]) && sb[idx[j]] == sb[idx[j + 1]] && idx[j] < idx[j + 1]);
-      const float ll = __ldg(row + lastid), lb = sb[lastid];
-      for (unsigned left = kept; left; left &= left - 1) {
-        const int e0 = (__ffs(left) - 1) * size;
-        for (int e = e0; e < e0 + size; ++e) {
-          const float l = __ldg(row + e);
-          const float v = value(l, sb[e]);
-          bool chosen = false;
+        for (int j = 0; j + 1 < K; ++j)
+          if (j + 1 < p.k && val[j + 1] > -INFINITY && !apart(val[j], val[j + 1])) doubt |= !same(idx[j], idx[j + 1]);
+        for (unsigned left = kept; left; left &= left - 1) {
+          const int e0 = (__ffs(left) - 1) * size;
+          for (int e = e0; e < e0 + size; ++e) {
+            const float v = value(col[e * S], sb[e]);
+            if (v > -INFINITY && !apart(lastv, v)) {
+              bool chosen = false;
 #pragma unroll
-          for (int j = 0; j < K; ++j) chosen |= j < p.k && idx[j] == e;
-          if (!chosen && v > -INFINITY && !apart(lastv, v)) doubt |= !(l == ll && sb[e] == lb && lastid < e);
+              for (int j = 0; j < K; ++j) chosen |= j < p.k && idx[j] == e;
+              if (!chosen) doubt |= !same(lastid, e);
+            }
+          }
         }
       }
-    }
-    doubt = doubt && live;
-    // weights of the chosen, in order
-    float w[K];
-    {
-      float m = -FLT_MAX, sum = 0.f;
+      // weights of the chosen, in order: from the scores where the tile holds them
+      float w[K], sum = 0.f, most = -FLT_MAX;
 #pragma unroll
       for (int j = 0; j < K; ++j) {
         if (j >= p.k || !(val[j] > -INFINITY)) idx[j] = -1;
-        w[j] = idx[j] < 0 ? 0.f : fminf(p.groups > 1 ? __ldg(row + idx[j]) : col[idx[j] * S], FLT_MAX);
+        w[j] = idx[j] < 0 ? 0.f : col[idx[j] * S];
+        most = idx[j] < 0 ? most : fmaxf(most, w[j]);
       }
+      if (p.groups > 1) {
+        // scores near the smallest floats share out the scale in 64 bits
+        hard |= p.renormalise && lastid >= 0 && most < 1e-30f;
+      } else if (SIGMOID || (BY_LOGIT && p.sigmoid)) {
+        most = p.renormalise ? fminf(most, 0.f) : 0.f;
 #pragma unroll
-      for (int j = 0; j < K; ++j)
-        if (idx[j] >= 0) m = fmaxf(m, w[j]);
-      if (SIGMOID || (BY_LOGIT && p.sigmoid)) {
-        m = p.renormalise ? fminf(m, 0.f) : 0.f;
-#pragma unroll
-        for (int j = 0; j < K; ++j)
-          if (idx[j] >= 0)
-            w[j] = w[j] > 0.f || !p.renormalise ? __fdividef(1.f, 1.f + expf(-w[j]))
-                                                : __fdividef(expf(w[j] - m), 1.f + expf(w[j]));
+        for (int j = 0; j < K; ++j) {
+          const float x = fminf(w[j], FLT_MAX);
+          const float a = x > 0.f || !p.renormalise ? __fdividef(1.f, 1.f + expf(-x))
+                                                    : __fdividef(expf(x - most), 1.f + expf(x));
+          w[j] = idx[j] < 0 ? 0.f : a;
+        }
       } else {
-        m = p.renormalise ? m : top;
+        most = p.renormalise ? fminf(most, FLT_MAX) : top;
 #pragma unroll
-        for (int j = 0; j < K; ++j)
-          if (idx[j] >= 0) w[j] = expf(w[j] - m);
+        for (int j = 0; j < K; ++j) {
+          const float a = expf(fminf(w[j], FLT_MAX) - most);
+          w[j] = idx[j] < 0 ? 0.f : a;
+        }
       }
 #pragma unroll
-      for (int j = 0; j < K; ++j)
-        if (idx[j] >= 0) sum += w[j];
-      const float f = !p.renormalise ? (p.sigmoid ? p.scale : p.scale * over) : sum > 0.f ? p.scale / sum : 0.f;
+      for (int j = 0; j < K; ++j) sum += w[j];
+      // a softmax's scores are divided by their sum already where groups were scored
+      const float f = p.renormalise                   ? (sum > 0.f ? p.scale / sum : 0.f)
+                      : p.sigmoid || p.groups > 1 ? p.scale
+                                                      : p.scale * over;
 #pragma unroll
-      for (int j = 0; j < K; ++j) w[j] = idx[j] >= 0 ? w[j] * f : 0.f;
-    }
-    if (live) {
-      if (!doubt) {
+      for (int j = 0; j < K; ++j) w[j] *= f;
+      doubt = (doubt || hard) && live;
+      if (live && !doubt) {
         if (K % 4 == 0 && p.k == K) {
 #pragma unroll
           for (int j = 0; j + 3 < K; j += 4) {
@@ -730,26 +727,108 @@ __global__ void __launch_bounds__(2 * kRows) route_thread_kernel(
               if (weights) weights[t * p.k + j] = w[j];
             }
         }
+      }
+      // gates: the chosen's weights to the tile, their places to a mask of 128 bits
+      unsigned chosen[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < K; ++j)
-          if (idx[j] >= 0) {
-            if (gates) gates[(int64_t)idx[j] * ld + t] = w[j];
-            if (counts) atomicAdd(hist + idx[j], 1);
+      for (int j = 0; j < K; ++j)
+        if (idx[j] >= 0 && live && !doubt) {
+          col[idx[j] * S] = w[j];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) chosen[q] |= idx[j] >> 5 == q ? 1u << (idx[j] & 31) : 0u;
+          if (counts) atomicAdd(hist + idx[j], 1);
+        }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) skept[q * kRows + tid] = chosen[q];
+      __syncwarp();
+      for (unsigned left = __ballot_sync(kAll, doubt); left; left &= left - 1) {
+        const int from_lane = __ffs(left) - 1, r = (tid & ~31) + from_lane;
+        const float* rowr = logits + (t0 + r) * N;
+        const float* colr = tile + r;
+        const float lastr = __shfl_sync(kAll, lastv, from_lane);
+        const unsigned keptr = __shfl_sync(kAll, kept, from_lane);
+        const float topr = __shfl_sync(kAll, top, from_lane), overr = __shfl_sync(kAll, over, from_lane);
+        // the experts that may be among the k best: one a lane
+        int* cand = reinterpret_cast<int*>(exact + (tid >> 5) * N);
+        int m = 0;
+        if (!__shfl_sync(kAll, (int)hard, from_lane)) {
+#pragma unroll 1
+          for (int e0 = 0; e0 < N; e0 += 32) {
+            const int e = e0 + lane;
+            float v = -INFINITY;
+            if (e < N && keptr >> (e / size) & 1) {
+              const float x = colr[e * S];
+              v = BY_LOGIT ? (there(x) ? fminf(x, FLT_MAX) : -INFINITY)
+                           : biased(p.groups > 1 ? x
+                                    : !there(x)  ? -1.f
+                                    : SIGMOID    ? quick_sigmoid(x)
+                                                 : quick_exp(fminf(x, FLT_MAX) - topr) * overr,
+                                    sb[e]);
+            }
+            const bool may = v > -INFINITY && !apart(lastr, v);
+            const unsigned who = __ballot_sync(kAll, may);
+            const int at = m + __popc(who & ((1u << lane) - 1));
+            if (may && at < 32) cand[at] = e;
+            m += __popc(who);
           }
+          __syncwarp();
+        }
+        int id;
+        float wj;
+        if (m >= 1 && m <= 32) {
+          const int e = lane < m ? cand[lane] : 0;
+          const double l = (double)fminf(__ldg(rowr + e), FLT_MAX);
+          double v = l, total64 = 0.0;
+          if (!BY_LOGIT) {
+            if (!SIGMOID) {
+#pragma unroll 1
+              for (int q = lane; q < N; q += 32) {
+                const float x = __ldg(rowr + q);
+                if (there(x)) total64 += exp_64((double)fminf(x, FLT_MAX) - (double)topr);
+              }
+              total64 = warp_sum(total64);
+            }
+            const double x = exp_64(SIGMOID ? -l : l - (double)topr);
+            v = (SIGMOID ? 1.0 / (1.0 + x) : x / total64) + (bias ? (double)__ldg(bias + e) : 0.0);
+          }
+          int rank = 0;
+#pragma unroll 1
+          for (int c = 0; c < m; ++c) {
+            const double other = __shfl_sync(kAll, v, c);
+            rank += other > v || (other == v && c < lane);  // candidates ascend
+          }
+          __syncwarp();
+          if (lane < m) cand[rank] = e;
+          __syncwarp();
+          id = lane < p.k && lane < m ? cand[lane] : -1;
+          __syncwarp();
+          wj = row_weight(p, id, id >= 0 ? fminf(__ldg(rowr + id), FLT_MAX) : 0.f, topr, overr);
+        } else {
+          route_row(&p, rowr, bias, exact + (tid >> 5) * N, &id, &wj);
+        }
+        if (lane < p.k) {
+          if (ids) ids[(t0 + r) * p.k + lane] = id;
+          if (weights) weights[(t0 + r) * p.k + lane] = wj;
+          if (id >= 0) {
+            tile[id * S + r] = wj;
+            atomicOr(skept + (id >> 5) * kRows + r, 1u << (id & 31));
+            if (counts) atomicAdd(hist + id, 1);
+          }
+        }
       }
     }
-    __syncwarp();
-    for (unsigned left = __ballot_sync(kAll, doubt); left; left &= left - 1) {
-      const int64_t tr = t0 + (tid & ~31) + __ffs(left) - 1;
-      int id;
-      float wj;
-      route_row<kThreadExperts / 32>(p, logits + tr * N, bias, &id, &wj);
-      if (lane < p.k) {
-        if (ids) ids[tr * p.k + lane] = id;
-        if (weights) weights[tr * p.k + lane] = wj;
-        if (id >= 0) {
-          if (counts) atomicAdd(hist + id, 1);
-          if (gates) gates[(int64_t)id * ld + tr] = wj;
+    if (gates) {  // each half writes half of the experts, a warp 32 rows of one expert
+      __syncthreads();
+      if (live) {
+        const int e0 = half * ((N + 1) / 2), e1 = half ? N : (N + 1) / 2;
+        float* out = gates + t0 + e0 * ld;
+        unsigned bits[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) bits[q] = skept[q * kRows + tid];
+#pragma unroll 8
+        for (int e = e0; e < e1; ++e, out += ld) {
+          const unsigned word = e < 64 ? (e < 32 ? bits[0] : bits[1]) : (e < 96 ? bits[2] : bits[3]);
+          out[tid] = word >> (e & 31) & 1 ? col[e * S] : 0.f;
         }
       }
     }
@@ -990,7 +1069,7 @@ template <int K>
 cudaError_t forward_threads(const RouteSpec& p, int64_t n, const float* logits, const float* bias, const RouteOut& o,
                             cudaStream_t s) {
   const int swap_rows = std::max(K + 1, p.groups > 1 ? 4 * p.groups : 2);
-  const size_t shared = sizeof(float) * ((size_t)(kRows + 1) * p.n + 2 * p.n + 4 + (size_t)(1 + swap_rows) * kRows);
+  const size_t shared = sizeof(float) * ((size_t)(kRows + 1) * p.n + 10 * p.n + 4 + (size_t)(4 + swap_rows) * kRows);
   const int64_t grid = std::min<int64_t>((n + kRows - 1) / kRows, kSms * 64);
   auto kernel = !bias && p.groups == 1 ? route_thread_kernel<K, false, true>
                 : p.sigmoid            ? route_thread_kernel<K, true, false>
