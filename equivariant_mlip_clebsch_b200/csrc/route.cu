@@ -851,7 +851,7 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
 constexpr int64_t kWholeRows = 1 << 22;  // values of an array
 
 template <int K>
-__global__ void __launch_bounds__(kRows) route_chosen_backward_kernel(
+__global__ void __launch_bounds__(2 * kRows, K <= 8 ? 5 : 2) route_chosen_backward_kernel(
     RouteSpec p, int64_t n, const float* __restrict__ logits, const int32_t* __restrict__ ids,
     const float* __restrict__ grad_weights, const float* __restrict__ grad_gates, int64_t ld,
     float* __restrict__ grad_logits, unsigned magic) {
@@ -859,16 +859,16 @@ __global__ void __launch_bounds__(kRows) route_chosen_backward_kernel(
   grid_launch_dependents();
   extern __shared__ float4 smem4[];
   float* smem = reinterpret_cast<float*>(smem4);
-  const int N = p.n, tid = threadIdx.x, R = blockDim.x, odd = N | 1;
+  const int N = p.n, R = blockDim.x / 2, half = threadIdx.x / R, tid = threadIdx.x - half * R, odd = N | 1;
   const bool whole = N <= 16 * p.k && n * N >= kWholeRows;
   for (int64_t t0 = (int64_t)blockIdx.x * R; t0 < n; t0 += (int64_t)gridDim.x * R) {
     const int rows = (int)min((int64_t)R, n - t0);
-    const bool live = tid < rows;
+    const bool live = tid < rows, mine = live && !half;  // the second half helps to move whole rows
     const int64_t t = t0 + tid;
     int id[K];
     float l[K], d[K];
 #pragma unroll
-    for (int j = 0; j < K; ++j) id[j] = live && j < p.k ? __ldg(ids + t * p.k + j) : -1;
+    for (int j = 0; j < K; ++j) id[j] = mine && j < p.k ? __ldg(ids + t * p.k + j) : -1;
     if (!whole) {
 #pragma unroll
       for (int j = 0; j < K; ++j) {
@@ -879,11 +879,12 @@ __global__ void __launch_bounds__(kRows) route_chosen_backward_kernel(
       __syncthreads();  // the tile of the round before is written out
     } else {
       __syncthreads();
-      if (grad_gates) {  // expert e of this row at smem[e R + tid]: only this thread's
-        const float* src = grad_gates + t0;
+      if (grad_gates) {  // expert e of this row at smem[e R + tid]
+        const float* src = grad_gates + t0 + half * ld;
         if (live)
 #pragma unroll 8
-          for (int e = 0; e < N; ++e, src += ld) smem[e * R + tid] = __ldg(src + tid);
+          for (int e = half; e < N; e += 2, src += 2 * ld) smem[e * R + tid] = __ldg(src + tid);
+        __syncthreads();
       }
 #pragma unroll
       for (int j = 0; j < K; ++j) d[j] = (unsigned)id[j] < (unsigned)N && grad_gates ? smem[id[j] * R + tid] : 0.f;
@@ -891,7 +892,7 @@ __global__ void __launch_bounds__(kRows) route_chosen_backward_kernel(
       const float* src = logits + t0 * N;
       if (N % 4 == 0) {
 #pragma unroll 4
-        for (int i = tid * 4; i < rows * N; i += R * 4) {
+        for (int i = threadIdx.x * 4; i < rows * N; i += R * 8) {
           const float4 f = __ldg(reinterpret_cast<const float4*>(src + i));
           const int r = (int)__umulhi(i, magic);
           float* dst = smem + r * odd + i - r * N;
@@ -902,7 +903,7 @@ __global__ void __launch_bounds__(kRows) route_chosen_backward_kernel(
         }
       } else {
 #pragma unroll 4
-        for (int i = tid; i < rows * N; i += R) {
+        for (int i = threadIdx.x; i < rows * N; i += 2 * R) {
           const int r = N == 1 ? i : (int)__umulhi(i, magic);
           smem[r * odd + i - r * N] = __ldg(src + i);
         }
@@ -912,9 +913,9 @@ __global__ void __launch_bounds__(kRows) route_chosen_backward_kernel(
       for (int j = 0; j < K; ++j) l[j] = (unsigned)id[j] < (unsigned)N ? smem[tid * odd + id[j]] : -FLT_MAX;
       __syncthreads();
     }
-    for (int i = tid; i < (rows * N + 3) / 4; i += R) smem4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = threadIdx.x; i < (rows * N + 3) / 4; i += 2 * R) smem4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     __syncthreads();
-    if (live) {
+    if (mine) {
       float* out = smem + tid * N;
 #pragma unroll
       for (int j = 0; j < K; ++j) {
@@ -954,8 +955,8 @@ __global__ void __launch_bounds__(kRows) route_chosen_backward_kernel(
     }
     __syncthreads();
     float* dst = grad_logits + t0 * N;
-    for (int i = tid; i < rows * N / 4; i += R) reinterpret_cast<float4*>(dst)[i] = smem4[i];
-    for (int i = (rows * N & ~3) + tid; i < rows * N; i += R) dst[i] = smem[i];
+    for (int i = threadIdx.x; i < rows * N / 4; i += 2 * R) reinterpret_cast<float4*>(dst)[i] = smem4[i];
+    for (int i = (rows * N & ~3) + threadIdx.x; i < rows * N; i += 2 * R) dst[i] = smem[i];
   }
 }
 
@@ -1082,7 +1083,7 @@ template <int K>
 cudaError_t backward_chosen(const RouteSpec& p, int64_t n, const float* logits, const int32_t* ids, const float* gw,
                             const float* gg, int64_t ld, float* out, cudaStream_t s) {
   const unsigned rows = p.n <= 64 ? kRows : p.n <= 256 ? 64 : 32;  // tiles of 33 to 66 KB
-  return launch_dependent(route_chosen_backward_kernel<K>, std::min<int64_t>((n + rows - 1) / rows, kSms * 64), rows,
+  return launch_dependent(route_chosen_backward_kernel<K>, std::min<int64_t>((n + rows - 1) / rows, kSms * 64), 2 * rows,
                           sizeof(float) * rows * (p.n | 1), s, p, n, logits, ids, gw, gg, ld, out, divide_by(p.n));
 }
 
