@@ -536,14 +536,14 @@ class LayerNorm:
         except Exception:
             pass
 
-    def _new(self, x, *shape):
+    def _new(self, x, shape):
         return x.new_empty(shape) if x.dtype is _types()["f32"] else x.new_empty(shape, dtype=_types()["f32"])
 
     def _like(self, x, n):
         """A new [n, D] array for x (empty_like is the cheaper call)."""
         if x.dtype is _types()["f32"] and x.dim() == 2 and x.shape[1] == self.d:
             return _torch().empty_like(x)
-        return self._new(x, n, self.d)
+        return self._new(x, (n, self.d))
 
     def forward(self, x, weight=None, bias=None, out=None, stream=None):
         n, dev = x.shape[0], x.device

@@ -380,7 +380,8 @@ cgtp_status cgtp_norm_forward(cgtp_norm norm, int64_t n, const float* x, const f
                               const float* bias, float* y, cgtp_stream stream);
 
 /* Bytes of device workspace that the two calls below need for n rows
- * (256-byte aligned; nothing in it needs initialising or outlives a call).
+ * (256-byte aligned; nothing in it needs initialising or outlives a call;
+ * calls that may run at the same time need one each).
  * Errors: NULL, SIZE. */
 cgtp_status cgtp_norm_workspace_size(cgtp_norm norm, int64_t n, size_t* bytes);
 

@@ -300,3 +300,25 @@ def test_gradient_of_the_gradient_by_differences(dev):
     # truncation h^2 S''' / 6, rounding ~ u sqrt(n D) |S terms| / h: both below 1e-2 of the terms' norm
     scale = sum((p.double() * q.double()).norm().item() for p, q in ((gg, dirs["g"]), (gx, dirs["x"]), (gw, dirs["w"])))
     assert abs(num - got) < 1e-2 * scale
+
+
+def test_offsets_beyond_32_bits(dev):
+    """2.2e9 values an array: the last rows equal the same rows alone."""
+    norm = C().LayerNorm("61x0e+1x1o", EPS)
+    n = 34_400_001  # x 64 > 2^31
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(1)
+    tail = torch.randn(4000, 64, device=dev, generator=gen)
+    w = torch.randn(62, device=dev, generator=gen)
+    x = torch.zeros(n, 64, device=dev)
+    x[-4000:] = tail
+    y = norm.forward(x, w)
+    assert torch.equal(y[-4000:], norm.forward(tail, w))
+    del y
+    g = torch.zeros(n, 64, device=dev)
+    g[-4000:] = 2 * tail
+    dx, dw, db = norm.backward(x, w, g)
+    rx, rw, rb = norm.backward(tail, w, 2 * tail)
+    assert torch.equal(dx[-4000:], rx) and not dx[:1000].any()
+    for a, b in ((dw, rw), (db, rb)):  # the same terms, added in another order: 780 u of their magnitudes
+        assert (a - b).abs().max().item() <= 2 * (K + 700) * U * 4000 * 64

@@ -264,3 +264,59 @@ def test_gradient_by_differences(dev):
             # rounding 160 u |w| |c| / h <= 5e-3 a row at |w| <= 1, |c| ~ 2; truncation h^2 ~ 4e-6 of third derivatives
             assert (num - d)[keep].abs().max().item() < 2e-2
             assert ((num - d)[keep].norm() / d[keep].norm()).item() < 5e-3
+
+
+def test_offsets_beyond_32_bits(dev):
+    """2.2e9 logits and gates: the last rows equal the same rows alone."""
+    n, E, k, m = 34_400_001, 64, 4, 3001
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(2)
+    tail, bias = torch.randn(m, E, device=dev, generator=gen), 0.1 * torch.randn(E, device=dev, generator=gen)
+    l = torch.full((n, E), LOW, device=dev)
+    l[-m:] = tail
+    r = C().Router(E, k, score="sigmoid", n_groups=8, top_groups=3)
+    ids, w, gates, counts = r.forward(l, bias)
+    one = r.forward(tail, bias)
+    assert torch.equal(ids[-m:], one[0]) and torch.equal(counts, one[3])
+    # few rows are decided by warps, many by threads: the same choice, weights apart by both bounds
+    assert ((w[-m:] - one[1]).abs() <= 320 * U * one[1]).all()
+    assert torch.equal(gates[:, -m:] != 0, one[2] != 0) and not gates[:, :1000].any()
+    assert (ids[:1000] == -1).all()
+    d = r.backward(l, ids, grad_gates=gates)
+    ref = r.backward(tail, one[0], grad_gates=one[2])
+    assert ((d[-m:] - ref).abs() <= 1e-5).all() and not d[:1000].any()
+
+
+def test_degenerate_rows_in_many(dev):
+    """20,000 rows of equal logits, a router not yet trained: the lowest indices,
+    on the form for many rows, with and without groups and bias."""
+    for E, kw in ((64, dict(k=8, score="sigmoid", n_groups=8, top_groups=4)), (64, dict(k=8)), (24, dict(k=3, score="sigmoid"))):
+        n = 20000
+        l = torch.zeros(n, E, device=dev)
+        for bias in (None, torch.zeros(E, device=dev)):
+            ids, w, gates, counts = C().Router(E, **kw).forward(l, bias)
+            oi, ow, _, _, _ = O.route_forward(np.zeros((1, E), np.float32), None if bias is None else np.zeros(E), **kw)
+            assert (ids.cpu().numpy() == oi).all()
+            assert np.abs(w.cpu().numpy() - ow).max() <= 160 * U
+            assert counts.sum().item() == n * kw["k"]
+
+
+@pytest.mark.parametrize("E,kw", ROUTES)
+def test_route_many_rows(E, kw, dev):
+    """The form for many rows against the oracle, whose rows are drawn from a
+    short list (the oracle goes row by row)."""
+    rng = np.random.default_rng(14)
+    base = (2 * rng.standard_normal((150, E))).astype(np.float32)
+    base[rng.random((150, E)) < 0.1] = -np.inf
+    base[7] = LOW
+    pick = rng.integers(0, 150, size=20001)
+    bias = (0.1 * rng.standard_normal(E)).astype(np.float32)
+    for b in (None, bias):
+        oi, ow, _, _, _ = O.route_forward(base, b, **kw)
+        ids, w, gates, counts = C().Router(E, **kw).forward(T(base[pick], dev), None if b is None else T(b, dev))
+        assert np.array_equal(ids.cpu().numpy(), oi[pick])
+        assert np.all(np.abs(w.cpu().numpy() - ow[pick]) <= 160 * U * ow[pick] + 1e-38)
+        assert np.array_equal(counts.cpu().numpy(), np.bincount(oi[pick][oi[pick] >= 0], minlength=E))
+        ref = np.zeros((E + 1, len(pick)), np.float32)
+        ref[np.where(oi[pick] < 0, E, oi[pick]), np.arange(len(pick))[:, None]] = w.cpu().numpy()
+        assert np.array_equal(gates.cpu().numpy(), ref[:E])
