@@ -296,18 +296,23 @@ __device__ __forceinline__ void norm_rows(const NormSeg& s, int o, int D, float 
       }
     group_sum<TLOG>(t, red, turn);
     const float r = rsqrtf(fmaf(t[0], inv, eps));
-    float along = 0.f, shift = 0.f, be = 0.f, rb = 0.f, rl = 0.f;
-    if constexpr (OP == kBackward) {  // grad_x = r (a - mean(a)) - (r al) xh
-      along = -r * (t[1] * inv * r);
-      shift = -r * ma;
-    }
-    if constexpr (OP == kDouble) {  // gx = r^2 (cx xh - be P a - al P h) + r (P k - de xh)
-      const float al = t[1] * inv * r, de = t[3] * inv * r, ga = t[4] * inv;
-      be = t[2] * inv * r;
-      along = r * r * (3.f * al * be - ga) - r * de;
-      rb = -r * r * be;
-      rl = -r * r * al;
-      shift = -(rb * ma + r * mk);
+    // From here on by xc = xh / r: what projects on xh is sum(z xc) xc / (sum(xc^2) + N
+    // eps), without the rounding of r twice.
+    float along = 0.f, shift = 0.f, ph = 0.f, rb = 0.f, rl = 0.f;
+    if constexpr (OP != kForward) {
+      const float over = 1.f / fmaf((float)len, eps, t[0]);
+      if constexpr (OP == kBackward) {  // grad_x = r (a - mean(a)) - r (sum(a xc) over) xc
+        along = -r * (t[1] * over);
+        shift = -r * ma;
+      }
+      if constexpr (OP == kDouble) {  // gx = r^2 (cx xh - be P a - al P h) + r (P k - de xh)
+        const float al = t[1] * inv * r, be = t[2] * inv * r, ga = t[4] * inv;
+        ph = -(t[2] * over);
+        along = r * (r * r * (3.f * al * be - ga) - t[3] * over);
+        rb = -r * r * be;
+        rl = -r * r * al;
+        shift = -(rb * ma + r * mk);
+      }
     }
 #pragma unroll
     for (int q = 0; q < V; ++q)
@@ -330,10 +335,9 @@ __device__ __forceinline__ void norm_rows(const NormSeg& s, int o, int D, float 
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int e = 4 * q + j;
-            const float xh = x[e] * r;
             gq[j] = g[e];
-            p[j] = g[e] * xh;
-            y[j] = fmaf(xh, along, CENTRED ? fmaf(g[e] * w[j], r, shift) : g[e] * w[j] * r);
+            p[j] = g[e] * (x[e] * r);
+            y[j] = fmaf(x[e], along, CENTRED ? fmaf(g[e] * w[j], r, shift) : g[e] * w[j] * r);
           }
           if (a.out) store4<SHIFT>(a.out + at + 4 * q * W, whole, some, y);
           if (dw) add_to(acc[q * T], make_float4(p[0], p[1], p[2], p[3]));
@@ -345,10 +349,10 @@ __device__ __forceinline__ void norm_rows(const NormSeg& s, int o, int D, float 
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int e = 4 * q + j;
-            const float xh = x[e] * r, jh = r * fmaf(-be, xh, h[e]);
+            const float xh = x[e] * r, jh = r * fmaf(ph, x[e], h[e]);
             y[j] = fmaf(w[j], jh, CENTRED ? fmaf(k[j], xh, b[j]) : k[j] * xh);
             const float c = fmaf(rb, w[j], r * k[j]);  // of g
-            const float lin = fmaf(rl, h[e], xh * along);
+            const float lin = fmaf(rl, h[e], x[e] * along);
             z[j] = fmaf(c, g[e], CENTRED ? lin + shift : lin);
             p[j] = g[e] * jh;
           }

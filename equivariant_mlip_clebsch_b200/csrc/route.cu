@@ -645,17 +645,20 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
         idx[j - 1] = wrong ? b : idx[j - 1];
       }
       bool close = false;
-      float lastv = -INFINITY;
+      float lastv = INFINITY;  // the smallest of the k first, also while two of them are the wrong way round
       int lastid = -1;
 #pragma unroll
       for (int j = 0; j < K; ++j) {
         const bool in = j < p.k && val[j] > -INFINITY;
-        close |= in && val[j + 1] > -INFINITY && !apart(val[j], val[j + 1]);
-        lastv = in ? val[j] : lastv;
+        close |= in && j + 1 < p.k && val[j + 1] > -INFINITY && !apart(val[j], val[j + 1]);
+        lastv = in ? fminf(lastv, val[j]) : lastv;
         lastid = in ? idx[j] : lastid;
       }
-      // Experts behind the last key: at most `outside`.  (Where fewer than k are
-      // left, the list holds them all and what is behind is -inf.)
+      // The rest of the list, which one pass need not have put in order, and the
+      // experts behind its last key, at most `outside`.  (Where fewer than k are left,
+      // the list holds them all and what is behind is -inf.)
+#pragma unroll
+      for (int j = 1; j <= K; ++j) close |= j >= p.k && lastid >= 0 && val[j] > -INFINITY && !apart(lastv, val[j]);
       close |= lastid >= 0 && outside > -INFINITY && val[K] > -INFINITY && !apart(lastv, outside);
       if (close && live && !hard) {
         auto same = [&](int a, int b) { return a < b && __ldg(row + a) == __ldg(row + b) && sb[a] == sb[b]; };
@@ -711,6 +714,7 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
                                                       : p.scale * over;
 #pragma unroll
       for (int j = 0; j < K; ++j) w[j] *= f;
+      if (p.renormalise && idx[0] >= 0 && (K == 1 || idx[K > 1] < 0)) w[0] = p.scale;  // a single one: not by rounding
       doubt = (doubt || hard) && live;
       if (live && !doubt) {
         if (K % 4 == 0 && p.k == K) {
@@ -931,27 +935,35 @@ __global__ void __launch_bounds__(2 * kRows, K <= 8 ? 5 : 2) route_chosen_backwa
           if (id[j] >= 0) m = fmaxf(m, l[j]);
         if (p.sigmoid) m = fminf(m, 0.f);
       }
-      // scores, the renormalised ones relative to exp(m); with one minus the sigmoid
+      // scores, the renormalised ones relative to exp(m) and then shares that add to
+      // one (a single one is 1, and its gradient 0)
+      float share[K];
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        share[j] = 0.f;
+        if (id[j] >= 0) {
+          const float x = l[j];
+          share[j] = !p.sigmoid                   ? expf(x - m)
+                     : x > 0.f || !p.renormalise ? 1.f / (1.f + expf(-x))
+                                                  : expf(x - m) / (1.f + expf(x));
+          sum += share[j];
+        }
+      }
+      if (p.renormalise) {
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+          if (id[j] >= 0) {
+            share[j] /= sum;
+            dot = fmaf(d[j], share[j], dot);
+          }
+      }
 #pragma unroll
       for (int j = 0; j < K; ++j)
         if (id[j] >= 0) {
-          const float x = l[j];
-          float sj;
-          if (!p.sigmoid) {
-            sj = expf(x - m);
-            l[j] = sj;
-          } else {
-            sj = x > 0.f || !p.renormalise ? 1.f / (1.f + expf(-x)) : expf(x - m) / (1.f + expf(x));
-            l[j] = sj / (1.f + expf(x));  // s (1 - s)
-          }
-          sum += sj;
-          dot = fmaf(d[j], sj, dot);
+          float x = p.scale * share[j] * (d[j] - dot);
+          if (p.sigmoid) x *= 1.f / (1.f + expf(l[j]));
+          out[id[j]] += x;
         }
-      const float over = p.renormalise ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
-      const float mean = p.renormalise ? dot * over : 0.f;
-#pragma unroll
-      for (int j = 0; j < K; ++j)
-        if (id[j] >= 0) out[id[j]] += p.scale * over * l[j] * (d[j] - mean);
     }
     __syncthreads();
     float* dst = grad_logits + t0 * N;

@@ -320,3 +320,35 @@ def test_route_many_rows(E, kw, dev):
         ref = np.zeros((E + 1, len(pick)), np.float32)
         ref[np.where(oi[pick] < 0, E, oi[pick]), np.arange(len(pick))[:, None]] = w.cpu().numpy()
         assert np.array_equal(gates.cpu().numpy(), ref[:E])
+
+
+@pytest.mark.parametrize("n", [150, 20001])
+@pytest.mark.parametrize("E,kw", [(75, dict(k=8, score="sigmoid", renormalise=False)), (75, dict(k=5)), (24, dict(k=1)),
+                                  (64, dict(k=8, score="sigmoid", n_groups=8, top_groups=4)),
+                                  (64, dict(k=3, score="softmax", n_groups=4, top_groups=2, group_best=1))])
+def test_route_of_close_logits(E, kw, n, dev):
+    """A dozen logits of every row a few steps of FP32 apart, in any order: the
+    FP32 forms meet wrong orders and decide them in 64 bits."""
+    rng = np.random.default_rng(15)
+    base = rng.standard_normal((150, E)).astype(np.float32)
+    for t in range(150):
+        at = rng.choice(E, 12, replace=False)
+        base[t, at] = 3 + rng.integers(0, (4, 40, 400)[t % 3], 12) * np.float32(2.0 ** -22)
+    pick = np.arange(n) % 150
+    for b in (None, np.full(E, 0.125, np.float32), (1e-7 * rng.standard_normal(E)).astype(np.float32)):
+        oi, ow, _, _, _ = O.route_forward(base, b, **kw)
+        ids, w, _, _ = C().Router(E, **kw).forward(T(base[pick], dev), None if b is None else T(b, dev))
+        assert np.array_equal(ids.cpu().numpy(), oi[pick])
+        assert np.all(np.abs(w.cpu().numpy() - ow[pick]) <= 160 * U * ow[pick] + 1e-38)
+
+
+def test_gradient_of_a_single_choice_is_zero(dev):
+    """Renormalised, one expert's weight is the scale whatever its logit."""
+    rng = np.random.default_rng(16)
+    for score in ("softmax", "sigmoid"):
+        for E, n in ((5, 300), (64, 70000)):
+            l = T(rng.standard_normal((n, E)).astype(np.float32), dev)
+            r = C().Router(E, 1, score=score, scale=2.5)
+            ids, w, _, _ = r.forward(l)
+            assert (w == 2.5).all()
+            assert not r.backward(l, ids, torch.randn_like(w)).any()
