@@ -824,15 +824,17 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
     if (gates) {  // each half writes half of the experts, a warp 32 rows of one expert
       __syncthreads();
       if (live) {
-        const int e0 = half * ((N + 1) / 2), e1 = half ? N : (N + 1) / 2;
+        const int mid = (N / 2 + 7) / 8 * 8, e0 = half ? mid : 0, e1 = half ? N : min(mid, N);
         float* out = gates + t0 + e0 * ld;
-        unsigned bits[4];
+        for (int e = e0; e < e1; e += 8) {  // eights do not cross a word of the mask
+          const unsigned bits = skept[(e >> 5) * kRows + tid] >> (e & 31);
+          const float* from_tile = col + e * S;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) bits[q] = skept[q * kRows + tid];
-#pragma unroll 8
-        for (int e = e0; e < e1; ++e, out += ld) {
-          const unsigned word = e < 64 ? (e < 32 ? bits[0] : bits[1]) : (e < 96 ? bits[2] : bits[3]);
-          out[tid] = word >> (e & 31) & 1 ? col[e * S] : 0.f;
+          for (int j = 0; j < 8; ++j)
+            if (e + j < e1) {
+              out[tid] = bits & 1u << j ? from_tile[j * S] : 0.f;
+              out += ld;
+            }
         }
       }
     }
