@@ -445,20 +445,29 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
   const int size = N / p.groups, split = (size + 1) / 2;
   const int from = half ? split : 0, to = half ? size : split;  // this thread's part of a group
   const bool fours = size % 8 == 0;                             // both parts are whole fours
+  // a thread's float4s of a tile are 8 kRows values apart: so many rows and columns
+  const int fill_r = N == 1 ? 0 : (int)__umulhi(threadIdx.x * 4, magic), fill_c = threadIdx.x * 4 - fill_r * N;
+  const int step_c = 8 * kRows % N, step_at = step_c * S + 8 * kRows / N;
   for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < n; t0 += (int64_t)gridDim.x * kRows) {
     const int rows = (int)min((int64_t)kRows, n - t0);
     __syncthreads();  // the tile of the round before is read
     const float* src = logits + t0 * N;  // rows N values from a 16-byte border
     if (N % 4 == 0) {
-#pragma unroll 8
+      int c = fill_c;
+      float* dst = tile + c * S + fill_r;
+#pragma unroll 4
       for (int i = threadIdx.x * 4; i < rows * N; i += 8 * kRows) {
         const float4 f = __ldg(reinterpret_cast<const float4*>(src + i));
-        const int r = (int)__umulhi(i, magic);
-        float* dst = tile + (i - r * N) * S + r;
         dst[0] = f.x;
         dst[S] = f.y;
         dst[2 * S] = f.z;
         dst[3 * S] = f.w;
+        c += step_c;
+        dst += step_at;
+        if (c >= N) {
+          c -= N;
+          dst -= N * S - 1;
+        }
       }
     } else {
 #pragma unroll 8
@@ -528,8 +537,11 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
         float* c = col + (g * size + from) * S;
         const float* b = sb + g * size + from;
         auto look = [&](float* at, float bi) {
-          const float s = score(*at), v = biased(s, bi);
-          *at = s;  // from here on the tile holds the scores
+          const float l = *at;
+          const float s = SIGMOID ? quick_sigmoid(l) : quick_exp(fminf(l, FLT_MAX) - top) * over;
+          const bool in = there(l);
+          const float v = in ? s + bi : -INFINITY;
+          *at = in ? s : -1.f;  // from here on the tile holds the scores
           b2 = fmaxf(b2, fminf(b1, v));
           b1 = fmaxf(b1, v);
         };
@@ -644,22 +656,25 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
         idx[j] = wrong ? idx[j - 1] : b;
         idx[j - 1] = wrong ? b : idx[j - 1];
       }
-      bool close = false;
-      float lastv = INFINITY;  // the smallest of the k first, also while two of them are the wrong way round
+      // The smallest gap: inside the k first, and from the smallest of them (also
+      // while two are the wrong way round) to the rest of the list, which one pass need
+      // not have put in order, and to the experts behind its last key, at most
+      // `outside`.  (Where fewer than k are left, the list holds them all; a difference
+      // with -inf is inf or a NaN, which fminf drops.)
+      float lastv = INFINITY, gap = INFINITY, rest = val[K] > -INFINITY ? outside : -INFINITY;
       int lastid = -1;
 #pragma unroll
-      for (int j = 0; j < K; ++j) {
+      for (int j = 0; j <= K; ++j) {
         const bool in = j < p.k && val[j] > -INFINITY;
-        close |= in && j + 1 < p.k && val[j + 1] > -INFINITY && !apart(val[j], val[j + 1]);
         lastv = in ? fminf(lastv, val[j]) : lastv;
         lastid = in ? idx[j] : lastid;
+        if (j > 0) gap = in ? fminf(gap, val[j - 1] - val[j]) : gap;
+        rest = j < p.k ? rest : fmaxf(rest, val[j]);
       }
-      // The rest of the list, which one pass need not have put in order, and the
-      // experts behind its last key, at most `outside`.  (Where fewer than k are left,
-      // the list holds them all and what is behind is -inf.)
-#pragma unroll
-      for (int j = 1; j <= K; ++j) close |= j >= p.k && lastid >= 0 && val[j] > -INFINITY && !apart(lastv, val[j]);
-      close |= lastid >= 0 && outside > -INFINITY && val[K] > -INFINITY && !apart(lastv, outside);
+      gap = fminf(gap, lastv - rest);
+      const float size_of = fmaxf(fabsf(val[0]), lastid >= 0 ? fabsf(lastv) : 0.f);
+      // every pair is closer to zero than size_of, or apart by more than it
+      const bool close = lastid >= 0 && !(BY_LOGIT ? gap > 0.f : gap > wide + 2.4e-7f * size_of);
       if (close && live && !hard) {
         auto same = [&](int a, int b) { return a < b && __ldg(row + a) == __ldg(row + b) && sb[a] == sb[b]; };
 #pragma unroll
@@ -739,11 +754,13 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
         if (idx[j] >= 0 && live && !doubt) {
           col[idx[j] * S] = w[j];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) chosen[q] |= idx[j] >> 5 == q ? 1u << (idx[j] & 31) : 0u;
+          for (int q = 0; q < 4; ++q)
+            if (32 * q < N) chosen[q] |= idx[j] >> 5 == q ? 1u << (idx[j] & 31) : 0u;
           if (counts) atomicAdd(hist + idx[j], 1);
         }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) skept[q * kRows + tid] = chosen[q];
+      for (int q = 0; q < 4; ++q)
+        if (32 * q < N) skept[q * kRows + tid] = chosen[q];
       __syncwarp();
       for (unsigned left = __ballot_sync(kAll, doubt); left; left &= left - 1) {
         const int from_lane = __ffs(left) - 1, r = (tid & ~31) + from_lane;
