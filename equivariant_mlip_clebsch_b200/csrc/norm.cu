@@ -194,8 +194,15 @@ __device__ __forceinline__ void add_to(float4& acc, const float4 v) {
 //
 // The group's size W = 2^TLOG is a constant, so that a thread's slots are
 // immediate offsets from one address an array: with W a variable the addresses
-// and conditions were four fifths of the instructions (73 a value instead of
-// about 20), and the backward was bound by their issue.
+// and conditions were four fifths of the instructions (73 a value, now 33), and the
+// backward was bound by their issue (Lmax 3 output: 93 us, now 74).
+//
+// What bounds it (B200, 6,144 rows of 256x0e+352x1o+384x2e+320x3o): the backward
+// moves its 403 MB at 5.5 TB/s, 84 % of the measured copy rate, with 32 warps an
+// SM; the forward of 768 rows of 52,864 columns 325 MB at 5.3 TB/s, 82 %; the
+// double backward of 6,144 x 704 (in L2) 86 MB in 20 us, held by the latency that
+// 16 warps an SM of 122 registers leave open (24 warps of 80 registers: 21 us, 32 of
+// 64: 24 us, for their spills).  Few rows cost their launches: 2 us and 7 us.
 template <int OP, int T, int V, bool SHIFT, bool CENTRED, int TLOG>
 __device__ __forceinline__ void norm_rows(const NormSeg& s, int o, int D, float eps, int64_t n, const NormArgs& a,
                                           bool dw, bool db, const float4* sw, const float4* s2, const float4* s3,

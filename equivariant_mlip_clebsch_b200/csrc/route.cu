@@ -342,7 +342,8 @@ __device__ __forceinline__ bool route_row_fast(const RouteSpec& p, const float* 
   return true;
 }
 
-// ---- forward, one warp a row, eight rows a CTA (few rows, many experts, k > 8)
+// ---- forward, one warp a row, eight rows a CTA (few rows, many experts, k > 8):
+// 6,910 x 74, k = 2: 18 us; with every row in 64 bits 23
 
 template <int PER>
 __global__ void __launch_bounds__(256) route_warp_kernel(const __grid_constant__ RouteSpec p, int64_t n, const float* __restrict__ logits,
@@ -417,6 +418,12 @@ __device__ __forceinline__ float key_top(int key, int mask) {
 // clears the row's gates while the first chooses the groups.  The tile lies
 // by experts, [expert][row], so that a thread's experts are constant offsets from
 // one address.
+//
+// What bounds it (B200, 172,050 x 64 in 8 groups, k = 8): 58 us for 99 MB, the issue of
+// some 5,900 instructions for 32 rows (62 % of the slots while it runs); phase by
+// phase 12 us to fill the tile, 9 the scores, 6 the groups, 5 the keys, 13 the list and
+// the weights, 7 the outputs, 6 the rows decided in 64 bits.  A warp a row in 64 bits
+// took 1,954 us.
 template <int K, bool SIGMOID, bool BY_LOGIT>
 __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
     const __grid_constant__ RouteSpec p, int64_t n, const float* __restrict__ logits, const float* __restrict__ bias,
@@ -868,8 +875,9 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
 // lines.  A chosen expert's logit and gate gradient are one sector each, and an SM
 // holds few requests of one sector: where the row is not much longer than its
 // choices and the arrays are large, the whole rows are read and the places picked
-// in shared memory (172,050 x 64, k = 8: 79 us by single sectors, 41 us whole;
-// 21,828 x 24, k = 6: 4.5 us by single sectors, 5.6 us whole).
+// in shared memory.  Measured, single sectors / whole, us: 172,050 x 64, k = 8: 79 /
+// 35; 60,000 x 128: 37 / 30; 60,000 x 64: 12.5 / 12.9; 10,000 x 64: 5.9 / 7.2.  What is
+// left of the first is latency: its 132 MB pass at 3.8 TB/s.
 
 constexpr int64_t kWholeRows = 1 << 22;  // values of an array
 
@@ -943,7 +951,10 @@ __global__ void __launch_bounds__(2 * kRows, K <= 8 ? 5 : 2) route_chosen_backwa
 #pragma unroll
       for (int j = 0; j < K; ++j) {
         if ((unsigned)id[j] < (unsigned)N && grad_weights) d[j] += __ldg(grad_weights + t * p.k + j);
-        if (!there(l[j])) id[j] = -1;  // out of range, out for the row, or NaN
+        if (!there(l[j])) {  // out of range, out for the row, or NaN
+          id[j] = -1;
+          d[j] = 0.f;
+        }
         l[j] = fminf(l[j], FLT_MAX);
       }
       float m = 0.f, sum = 0.f, dot = 0.f;
@@ -979,7 +990,13 @@ __global__ void __launch_bounds__(2 * kRows, K <= 8 ? 5 : 2) route_chosen_backwa
 #pragma unroll
       for (int j = 0; j < K; ++j)
         if (id[j] >= 0) {
-          float x = p.scale * share[j] * (d[j] - dot);
+          float x = d[j] - dot;
+          if (K <= 8 && p.renormalise) {  // pair by pair: where one share is nearly 1 its d and dot cancel
+            x = 0.f;
+#pragma unroll
+            for (int i = 0; i < K; ++i) x = fmaf(share[i], d[j] - d[i], x);
+          }
+          x *= p.scale * share[j];
           if (p.sigmoid) x *= 1.f / (1.f + expf(l[j]));
           out[id[j]] += x;
         }
@@ -993,6 +1010,7 @@ __global__ void __launch_bounds__(2 * kRows, K <= 8 ? 5 : 2) route_chosen_backwa
 
 // ---- backward of the softmax as it is, whose sum reaches every logit: L
 // lanes a row, lane i the experts i, i + L, ...; lane j also the row's j-th choice.
+// (34,244 x 16, k = 2: 5.2 us; by one thread a row over a tile 8.5.)
 
 template <int L, int PER>
 __global__ void __launch_bounds__(256) route_every_backward_kernel(
@@ -1149,7 +1167,12 @@ cudaError_t launch_backward(const RouteSpec& p, int64_t n, const float* logits, 
 
 cudaError_t launch_forward(const RouteSpec& p, int64_t n, const float* logits, const float* bias, const RouteOut& o,
                            cudaStream_t s) {
-  if (p.k <= kThreadK && p.n <= kThreadExperts && (n >= kSms * kRows || p.n <= 16)) {
+  // A thread's row is one long chain, whatever their number; warps take their rows
+  // side by side until the SMs are full.  Measured, threads / warps, us: 64 experts, k =
+  // 8: 1,000 rows 12.4 / 10.5, 4,000 12.4 / 20.5, 20,000 20.6 / 75; 128 experts, k = 8:
+  // 4,000 31 / 16, 10,000 31 / 31, 60,000 53 / 152; 32 experts, k = 2: 1,000 8.2 / 6.3,
+  // 4,000 8.3 / 10.4; 16 experts, k = 8: 1,000 9.7 / 8.2, 4,000 11.9 / 12.4.
+  if (p.k <= kThreadK && p.n <= kThreadExperts && n >= std::max(1500, p.n * p.n / 2)) {
     if (p.k == 1) return forward_threads<1>(p, n, logits, bias, o, s);
     if (p.k == 2) return forward_threads<2>(p, n, logits, bias, o, s);
     if (p.k <= 4) return forward_threads<4>(p, n, logits, bias, o, s);

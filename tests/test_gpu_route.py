@@ -85,7 +85,7 @@ ROUTES = [(4, dict(k=1, score="softmax", renormalise=False)), (16, dict(k=2, sco
 
 
 @pytest.mark.parametrize("E,kw", ROUTES)
-@pytest.mark.parametrize("n", [1, 3, 37, 300])
+@pytest.mark.parametrize("n", [1, 3, 37, 300, 1501])
 @pytest.mark.parametrize("bias", [False, True])
 def test_route_matches_the_oracle(E, kw, n, bias, dev):
     rng = np.random.default_rng(100 + n + E)
@@ -352,3 +352,21 @@ def test_gradient_of_a_single_choice_is_zero(dev):
             ids, w, _, _ = r.forward(l)
             assert (w == 2.5).all()
             assert not r.backward(l, ids, torch.randn_like(w)).any()
+
+
+def test_backward_ignores_the_gradient_of_what_is_out(dev):
+    """A NaN in the gradient at an id that is -1, or whose logit is masked, reaches nothing."""
+    rng = np.random.default_rng(17)
+    l = rng.standard_normal((6, 8)).astype(np.float32)
+    l[1, 2], l[2, 2], l[3, 2] = -np.inf, np.nan, LOW
+    ids = np.tile(np.array([[1, 2, 5]], np.int32), (6, 1))
+    ids[4, 1] = -1
+    gw = rng.standard_normal((6, 3)).astype(np.float32)
+    gw[1:5, 1] = np.nan
+    clean = np.where(np.isnan(gw), 0, gw).astype(np.float32)
+    for score in ("softmax", "sigmoid"):
+        for renormalise in (False, True):
+            r = C().Router(8, 3, score=score, renormalise=renormalise)
+            d = r.backward(T(l, dev), T(ids, dev), T(gw, dev)).cpu().numpy()
+            ref = O.route_backward(l, ids, clean, None, score, renormalise)
+            assert np.abs(d - ref).max() < 1e-6
