@@ -909,11 +909,14 @@ __global__ void __launch_bounds__(2 * kRows, K <= 8 ? 5 : 2) route_chosen_backwa
       }
       __syncthreads();  // the tile of the round before is written out
     } else {
+      // the logits' rows, one piece of memory, on their way while the gates' are read
+      if (N % 4 == 0 && threadIdx.x == 0)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(logits + t0 * N), "r"(rows * N * 4) : "memory");
       __syncthreads();
       if (grad_gates) {  // expert e of this row at smem[e R + tid]
         const float* src = grad_gates + t0 + half * ld;
         if (live)
-#pragma unroll 8
+#pragma unroll 16
           for (int e = half; e < N; e += 2, src += 2 * ld) smem[e * R + tid] = __ldg(src + tid);
         __syncthreads();
       }
@@ -922,7 +925,7 @@ __global__ void __launch_bounds__(2 * kRows, K <= 8 ? 5 : 2) route_chosen_backwa
       __syncthreads();
       const float* src = logits + t0 * N;
       if (N % 4 == 0) {
-#pragma unroll 4
+#pragma unroll 8
         for (int i = threadIdx.x * 4; i < rows * N; i += R * 8) {
           const float4 f = __ldg(reinterpret_cast<const float4*>(src + i));
           const int r = (int)__umulhi(i, magic);
