@@ -32,6 +32,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -885,7 +886,9 @@ cgtp_status cgtp_norm_create(const char* irreps, double eps, cgtp_norm* out) {
     std::vector<Irrep> v;
     std::string err;
     if (!parse_irreps(irreps, v, err)) return fail(CGTP_ERR_IRREPS_PARSE, err);
-    if (!((float)eps > 0.f) || !std::isfinite((float)eps)) return fail(CGTP_ERR_SIZE, "eps must be positive and finite");
+    // a normal float: the backward divides by the sum of squares plus N eps
+    if (!((float)eps >= FLT_MIN) || !std::isfinite((float)eps))
+      return fail(CGTP_ERR_SIZE, "eps must be a positive normal FP32 number");
     if (v.size() > kMaxBlocks) return fail(CGTP_ERR_SIZE, "more than 32 irreps blocks");
     NormTable t;
     std::memset(&t, 0, sizeof t);

@@ -366,7 +366,7 @@ typedef struct cgtp_norm_s* cgtp_norm;
 
 /* irreps as for cgtp_plan_create (l <= 6, multiplicities > 0, at most 32
  * blocks, the same (l, parity) may appear again: a block of its own);
- * eps > 0 and finite in FP32.  On failure *out is NULL.
+ * eps a positive normal FP32 number.  On failure *out is NULL.
  * Errors: NULL, IRREPS_PARSE, LMAX, SIZE (eps, too many or too wide blocks), OOM. */
 cgtp_status cgtp_norm_create(const char* irreps, double eps, cgtp_norm* out);
 cgtp_status cgtp_norm_destroy(cgtp_norm norm); /* NULL is accepted */

@@ -322,3 +322,15 @@ def test_offsets_beyond_32_bits(dev):
     assert torch.equal(dx[-4000:], rx) and not dx[:1000].any()
     for a, b in ((dw, rw), (db, rb)):  # the same terms, added in another order: 780 u of their magnitudes
         assert (a - b).abs().max().item() <= 2 * (K + 700) * U * 4000 * 64
+
+
+def test_zero_rows_with_the_smallest_eps(dev):
+    eps = float(np.finfo(np.float32).tiny)
+    norm = C().LayerNorm("8x0e+4x1o", eps)
+    x, g = torch.zeros(3, 20, device=dev), torch.ones(3, 20, device=dev)
+    assert not norm.forward(x).any()
+    dx, dw, _ = norm.backward(x, None, g)
+    assert torch.isfinite(dx).all() and not dw.any()
+    assert (dx[:, 8:] * eps ** 0.5 - 1).abs().max().item() <= 8 * U
+    gg, gx, gw = norm.double_backward(x, None, g, h_x=g)
+    assert torch.isfinite(gg).all() and not gw[:8].any()

@@ -13,7 +13,7 @@ torch = pytest.importorskip("torch")
 @pytest.mark.parametrize("irreps,eps,status", [
     ("16x0e+", 1e-5, PARSE), ("", 1e-5, PARSE), ("0x0e", 1e-5, PARSE), ("16x7e", 1e-5, LMAX),
     ("16x0e", 0.0, SIZE), ("16x0e", -1.0, SIZE), ("16x0e", float("nan"), SIZE), ("16x0e", float("inf"), SIZE),
-    ("16x0e", 1e-60, SIZE), ("+".join(["2x0e"] * 33), 1e-5, SIZE),
+    ("16x0e", 1e-60, SIZE), ("16x0e", 1e-40, SIZE), ("16x0e", 1e39, SIZE), ("+".join(["2x0e"] * 33), 1e-5, SIZE),
     ("+".join(["1000000x6e"] * 32) + "+8x0e", 1e-5, SIZE), ("+".join(["1048576x6e"] * 32), 1e-5, OK),
 ])
 def test_norm_create_refusals(irreps, eps, status):
