@@ -173,6 +173,16 @@ def _stream_of(dev, stream):
     return stream.cuda_stream
 
 
+def _new_on(stream, make):
+    """make(), which allocates, with the stream of the call as the current one:
+    what another stream writes must not be memory that the current one still
+    reads, or is given again before the call has run."""
+    if stream is None:
+        return make()
+    with _torch().cuda.stream(stream):
+        return make()
+
+
 def real_cg(l1: int, l2: int, l3: int) -> np.ndarray:
     C = np.zeros((2 * l1 + 1, 2 * l2 + 1, 2 * l3 + 1), dtype=np.float64)
     _check(_lib.cgtp_real_cg(l1, l2, l3, _np_ptr(C)))
@@ -548,7 +558,7 @@ class LayerNorm:
     def forward(self, x, weight=None, bias=None, out=None, stream=None):
         n, dev = x.shape[0], x.device
         if out is None:
-            out = self._like(x, n)
+            out = _new_on(stream, lambda: self._like(x, n))
         ptrs = _args(dev, (x, "x", n * self.d, "f32"), (weight, "weight", self.n_weight, "f32"),
                      (bias, "bias", self.n_bias, "f32"), (out, "out", n * self.d, "f32"))
         _check(_lib.cgtp_norm_forward(self._h, n, *ptrs, _stream_of(dev, stream)))
@@ -559,24 +569,26 @@ class LayerNorm:
         _check(_lib.cgtp_norm_workspace_size(self._h, n, ctypes.byref(b)))
         return b.value
 
-    def _ws(self, workspace, n, dev):
-        if workspace is None:
-            import torch
-            workspace = torch.empty(max(self.workspace_size(n), 256), dtype=torch.uint8, device=dev)
-        return _workspace(workspace, dev)
+    def _ws(self, workspace, n, dev, stream):
+        if workspace is not None:
+            return workspace
+        return _new_on(stream, lambda: _torch().empty(max(self.workspace_size(n), 256), dtype=_torch().uint8,
+                                                      device=dev))
 
     def backward(self, x, weight, grad_out, want=("x", "weight", "bias"), grads=None, workspace=None,
                  stream=None):
         """(grad_x, grad_weight, grad_bias) for grad_out = dL/dy."""
         n, dev = x.shape[0], x.device
         if grads is None:
-            grads = (self._like(x, n) if "x" in want else None, self._new(x, self.n_weight) if "weight" in want else None,
-                     self._new(x, self.n_bias) if "bias" in want else None)
+            grads = _new_on(stream, lambda: (self._like(x, n) if "x" in want else None,
+                                             self._new(x, self.n_weight) if "weight" in want else None,
+                                             self._new(x, self.n_bias) if "bias" in want else None))
         dx, dw, db = grads
         ptrs = _args(dev, (x, "x", n * self.d, "f32"), (weight, "weight", self.n_weight, "f32"),
                      (grad_out, "grad_out", n * self.d, "f32"), (dx, "grad_x", n * self.d, "f32"),
                      (dw, "grad_weight", self.n_weight, "f32"), (db, "grad_bias", self.n_bias, "f32"))
-        _check(_lib.cgtp_norm_backward(self._h, n, *ptrs, *self._ws(workspace, n, dev), _stream_of(dev, stream)))
+        workspace = self._ws(workspace, n, dev, stream)  # held until the launch
+        _check(_lib.cgtp_norm_backward(self._h, n, *ptrs, *_workspace(workspace, dev), _stream_of(dev, stream)))
         return dx, dw, db
 
     def double_backward(self, x, weight, grad_out, h_x=None, h_weight=None, h_bias=None,
@@ -586,15 +598,17 @@ class LayerNorm:
         cotangents are zero."""
         n, dev = x.shape[0], x.device
         if grads is None:
-            grads = (self._like(x, n) if "g" in want else None, self._like(x, n) if "x" in want else None,
-                     self._new(x, self.n_weight) if "weight" in want else None)
+            grads = _new_on(stream, lambda: (self._like(x, n) if "g" in want else None,
+                                             self._like(x, n) if "x" in want else None,
+                                             self._new(x, self.n_weight) if "weight" in want else None))
         gg, gx, gw = grads
         ptrs = _args(dev, (x, "x", n * self.d, "f32"), (weight, "weight", self.n_weight, "f32"),
                      (grad_out, "grad_out", n * self.d, "f32"), (h_x, "h_x", n * self.d, "f32"),
                      (h_weight, "h_weight", self.n_weight, "f32"), (h_bias, "h_bias", self.n_bias, "f32"),
                      (gg, "grad_grad_out", n * self.d, "f32"), (gx, "grad_x", n * self.d, "f32"),
                      (gw, "grad_weight", self.n_weight, "f32"))
-        _check(_lib.cgtp_norm_double_backward(self._h, n, *ptrs, *self._ws(workspace, n, dev),
+        workspace = self._ws(workspace, n, dev, stream)  # held until the launch
+        _check(_lib.cgtp_norm_double_backward(self._h, n, *ptrs, *_workspace(workspace, dev),
                                               _stream_of(dev, stream)))
         return gg, gx, gw
 
@@ -645,19 +659,22 @@ class Router:
             raise ValueError(f"{name}: rows overlap (stride {ld}, {n} columns)")
         return t.data_ptr(), ld
 
+    def _outs(self, logits, n, want):
+        f32, i32 = _types()["f32"], _types()["i32"]
+        e = lambda dtype, *shape: logits.new_empty(shape, dtype=dtype)
+        gates = e(f32, self.n_experts, -(-n // 4) * 4) if "gates" in want else None
+        if gates is not None and n % 4:
+            gates = gates[:, :n]
+        return (e(i32, n, self.k) if "ids" in want else None, e(f32, n, self.k) if "weights" in want else None,
+                gates, e(i32, self.n_experts) if "counts" in want else None)
+
     def forward(self, logits, bias=None, want=("ids", "weights", "gates", "counts"), outs=None, stream=None):
         """(ids [n, k] int32, weights [n, k], gates [n_experts, n], counts
         [n_experts] int32) of logits [n, n_experts].  The rows of gates are
         16-byte aligned (their stride is n rounded up to 4)."""
         n, dev = logits.shape[0], logits.device
         if outs is None:
-            f32, i32 = _types()["f32"], _types()["i32"]
-            e = lambda dtype, *shape: logits.new_empty(shape, dtype=dtype)
-            gates = e(f32, self.n_experts, -(-n // 4) * 4) if "gates" in want else None
-            if gates is not None and n % 4:
-                gates = gates[:, :n]
-            outs = (e(i32, n, self.k) if "ids" in want else None, e(f32, n, self.k) if "weights" in want else None,
-                    gates, e(i32, self.n_experts) if "counts" in want else None)
+            outs = _new_on(stream, lambda: self._outs(logits, n, want))
         ids, weights, gates, counts = outs
         pl, pb, pi, pw, pc = _args(dev, (logits, "logits", n * self.n_experts, "f32"),
                                    (bias, "bias", self.n_experts, "f32"), (ids, "ids", n * self.k, "i32"),
@@ -672,7 +689,7 @@ class Router:
         grad_gates [n_experts, n] (rows may be padded)."""
         n, dev = logits.shape[0], logits.device
         if grad_logits is None:
-            grad_logits = logits.new_empty((n, self.n_experts), dtype=_types()["f32"])
+            grad_logits = _new_on(stream, lambda: logits.new_empty((n, self.n_experts), dtype=_types()["f32"]))
         pl, pi, pw, po = _args(dev, (logits, "logits", n * self.n_experts, "f32"), (ids, "ids", n * self.k, "i32"),
                                (grad_weights, "grad_weights", n * self.k, "f32"),
                                (grad_logits, "grad_logits", n * self.n_experts, "f32"))
