@@ -406,6 +406,39 @@ __device__ __forceinline__ float key_top(int key, int mask) {
   return __int_as_float(i);
 }
 
+// A falling list of L = 2^i + 1 keys: the places from the back meet a falling list
+// b of n <= L from its front, and the larger ones, the best L of both, are put in
+// order (a bitonic merge whose first place stands alone).
+template <int L>
+__device__ __forceinline__ void merge_keys(int (&a)[L], const int* b, int n) {
+  auto meet = [&](int i, int j) {
+    const int most = max(a[i], a[j]);
+    a[j] = min(a[i], a[j]);
+    a[i] = most;
+  };
+#pragma unroll
+  for (int i = 0; i < n; ++i) a[L - 1 - i] = max(a[L - 1 - i], b[i]);
+  meet(0, L - 1);
+#pragma unroll
+  for (int m = (L - 1) / 2; m > 0; m /= 2)
+#pragma unroll
+    for (int i = 1; i < L; ++i)
+      if (((i - 1) & m) == 0) meet(i, i + m);
+}
+
+__device__ __forceinline__ void sort_four(int (&b)[4]) {
+  auto meet = [&](int i, int j) {
+    const int most = max(b[i], b[j]);
+    b[j] = min(b[i], b[j]);
+    b[i] = most;
+  };
+  meet(0, 1);
+  meet(2, 3);
+  meet(0, 2);
+  meet(1, 3);
+  meet(1, 2);
+}
+
 // A row's choice in FP32, by one thread.  Two compared values are off by at
 // most twice value_error against one another; where a decision is closer than that
 // the row is looked at again (two experts of equal logit and bias are in their
@@ -537,6 +570,20 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
         key[j] = a;
       }
     };
+    // four experts from e on; a long list takes them sorted (40 instructions for a
+    // list of nine, 72 one by one)
+    auto insert_four = [&](const float* c, int e) {
+      int x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = key_of(value(c[j * S], sb[e + j]), e + j, mask);
+      if constexpr (K >= 4) {
+        sort_four(x);
+        merge_keys(key, x, 4);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) insert(x[j]);
+      }
+    };
     if (p.groups > 1) {
       // the best two of every group, of each half
       for (int g = 0; g < p.groups; ++g) {
@@ -613,10 +660,7 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
         const int end = e + to - from;
         const float* c = col + e * S;
         if (fours) {
-          for (; e < end; e += 4, c += 4 * S) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) insert(key_of(value(c[j * S], sb[e + j]), e + j, mask));
-          }
+          for (; e < end; e += 4, c += 4 * S) insert_four(c, e);
         } else {
 #pragma unroll 1
           for (; e < end; ++e, c += S) insert(key_of(value(*c, sb[e]), e, mask));
@@ -625,10 +669,7 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
     } else {
       const float* c = col + from * S;
       if (fours) {
-        for (int e = from; e < to; e += 4, c += 4 * S) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) insert(key_of(value(c[j * S], sb[e + j]), e + j, mask));
-        }
+        for (int e = from; e < to; e += 4, c += 4 * S) insert_four(c, e);
       } else {
 #pragma unroll 1
         for (int e = from; e < to; ++e, c += S) insert(key_of(value(*c, sb[e]), e, mask));
@@ -640,8 +681,10 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
     }
     __syncthreads();
     if (!half) {
+      int other[K + 1];
 #pragma unroll
-      for (int j = 0; j <= K; ++j) insert(__float_as_int(swap[j * kRows + tid]));
+      for (int j = 0; j <= K; ++j) other[j] = __float_as_int(swap[j * kRows + tid]);
+      merge_keys(key, other, K + 1);
       // the values behind the keys, as they were compared
       float val[K + 1];
       int idx[K + 1];
