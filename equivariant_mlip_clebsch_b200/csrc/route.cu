@@ -585,11 +585,12 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
       }
     };
     if (p.groups > 1) {
-      // the best two of every group, of each half
-      for (int g = 0; g < p.groups; ++g) {
+      // the groups' scores, half of the groups by each half
+      const int mid = (p.groups + 1) / 2, last_group = half ? p.groups : mid;
+      for (int g = half ? mid : 0; g < last_group; ++g) {
         float b1 = -INFINITY, b2 = -INFINITY;
-        float* c = col + (g * size + from) * S;
-        const float* b = sb + g * size + from;
+        float* c = col + g * size * S;
+        const float* b = sb + g * size;
         auto look = [&](float* at, float bi) {
           const float l = *at;
           const float s = SIGMOID ? quick_sigmoid(l) : quick_exp(fminf(l, FLT_MAX) - top) * over;
@@ -599,8 +600,9 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
           b2 = fmaxf(b2, fminf(b1, v));
           b1 = fmaxf(b1, v);
         };
-        if (fours) {
-          for (int i = from; i < to; i += 4, c += 4 * S, b += 4) {
+        if (size % 4 == 0) {
+#pragma unroll 1
+          for (int i = 0; i < size; i += 4, c += 4 * S, b += 4) {
             const float4 bi = *reinterpret_cast<const float4*>(b);
             look(c, bi.x);
             look(c + S, bi.y);
@@ -609,25 +611,12 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
           }
         } else {
 #pragma unroll 1
-          for (int i = from; i < to; ++i, c += S, ++b) look(c, *b);
+          for (int i = 0; i < size; ++i, c += S, ++b) look(c, *b);
         }
-        float* at = swap + 2 * g * kRows + tid;
-        if (half) {
-          at[0] = b1;
-          at[kRows] = b2;
-        } else {
-          at[2 * p.groups * kRows] = b1;
-          at[(2 * p.groups + 1) * kRows] = b2;
-        }
+        swap[g * kRows + tid] = p.group_best == 2 && b2 > -INFINITY ? b1 + b2 : b1;
       }
       __syncthreads();
       if (!half) {
-        for (int g = 0; g < p.groups; ++g) {
-          float* at = swap + 2 * g * kRows + tid;
-          const float a1 = at[0], a2 = at[kRows], c1 = at[2 * p.groups * kRows], c2 = at[(2 * p.groups + 1) * kRows];
-          const float b1 = fmaxf(a1, c1), b2 = fmaxf(fminf(a1, c1), fmaxf(a2, c2));
-          at[0] = p.group_best == 2 && b2 > -INFINITY ? b1 + b2 : b1;
-        }
         kept = 0;
         float last = INFINITY;
         for (int r = 0; r < p.top_groups; ++r) {
@@ -635,7 +624,7 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
           int at = -1;
 #pragma unroll 4
           for (int g = 0; g < p.groups; ++g) {
-            const float x = swap[2 * g * kRows + tid];
+            const float x = swap[g * kRows + tid];
             if (x > best) {
               best = x;
               at = g;
@@ -644,12 +633,12 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
           if (at >= 0) {
             kept |= 1u << at;
             last = best;
-            swap[2 * at * kRows + tid] = -INFINITY;
+            swap[at * kRows + tid] = -INFINITY;
           }
         }
         float next = -INFINITY;
 #pragma unroll 4
-        for (int g = 0; g < p.groups; ++g) next = fmaxf(next, swap[2 * g * kRows + tid]);
+        for (int g = 0; g < p.groups; ++g) next = fmaxf(next, swap[g * kRows + tid]);
         hard = next > -INFINITY && !(last - next > 2.f * wide + 2.4e-7f * (fabsf(last) + fabsf(next)));
         skept[tid] = kept;
       }
@@ -1164,7 +1153,7 @@ cudaError_t forward_warps(const RouteSpec& p, int64_t n, const float* logits, co
 template <int K>
 cudaError_t forward_threads(const RouteSpec& p, int64_t n, const float* logits, const float* bias, const RouteOut& o,
                             cudaStream_t s) {
-  const int swap_rows = std::max(K + 1, p.groups > 1 ? 4 * p.groups : 2);
+  const int swap_rows = std::max(std::max(K + 1, 2), p.groups);
   const size_t shared = sizeof(float) * ((size_t)(kRows + 1) * p.n + 10 * p.n + 4 + (size_t)(4 + swap_rows) * kRows);
   const int64_t grid = std::min<int64_t>((n + kRows - 1) / kRows, kSms * 64);
   auto kernel = !bias && p.groups == 1 ? route_thread_kernel<K, false, true>
