@@ -386,10 +386,11 @@ __global__ void __launch_bounds__(256) route_warp_kernel(const __grid_constant__
 
 // ---- forward, one thread a row (many rows)
 
-constexpr int kRows = 128;           // rows of a CTA's tile
+// Rows of a CTA's tile.  64 / 128, us: 172,050 x 128, k = 8: 117 / 137; x 96: 84 / 90; x 64
+// in 8 groups: 49.5 / 49; 400,000 x 16, k = 2: 28.7 / 27.2.
+constexpr int kTile = 64;
 constexpr int kThreadExperts = 128;  // the widest row of this form
 constexpr int kThreadK = 8;
-
 
 // A key whose order as an integer is the value's, its low bits replaced so that of
 // equal values the lowest index is the largest; mask = 2^bits - 1 >= experts - 1.
@@ -452,13 +453,12 @@ __device__ __forceinline__ void sort_four(int (&b)[4]) {
 // by experts, [expert][row], so that a thread's experts are constant offsets from
 // one address.
 //
-// What bounds it (B200, 172,050 x 64 in 8 groups, k = 8): 58 us for 99 MB, the issue of
-// some 5,900 instructions for 32 rows (62 % of the slots while it runs); phase by
-// phase 12 us to fill the tile, 9 the scores, 6 the groups, 5 the keys, 13 the list and
-// the weights, 7 the outputs, 6 the rows decided in 64 bits.  A warp a row in 64 bits
-// took 1,954 us.
+// What bounds it (B200, 172,050 x 64 in 8 groups, k = 8): 51 us for 99 MB, the issue of
+// some 5,200 instructions for 32 rows (62 % of the slots while an SM is full), the
+// barriers at which a second half waits for the list of the first, and the last of
+// 2.3 waves.  A warp a row in 64 bits took 1,954 us.
 template <int K, bool SIGMOID, bool BY_LOGIT>
-__global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
+__global__ void __launch_bounds__(2 * kTile, 512 / kTile) route_thread_kernel(
     const __grid_constant__ RouteSpec p, int64_t n, const float* __restrict__ logits, const float* __restrict__ bias,
     int32_t* __restrict__ ids, float* __restrict__ weights, float* __restrict__ gates, int64_t ld,
     int32_t* __restrict__ counts, unsigned magic) {
@@ -466,15 +466,15 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
   grid_launch_dependents();
   extern __shared__ float4 smem4[];
   float* smem = reinterpret_cast<float*>(smem4);
-  constexpr int S = kRows + 1;  // odd: neither filling nor reading meets one bank
-  const int tid = threadIdx.x & (kRows - 1), half = threadIdx.x / kRows, lane = tid & 31, N = p.n;
-  double* exact = reinterpret_cast<double*>(smem4);    // [4][N] of the warps that decide
-  float* sb = smem + 8 * N;                            // [N] bias, in whole float4s
-  float* tile = sb + (N + 3) / 4 * 4;                  // [N][S]
-  int* hist = reinterpret_cast<int*>(tile + N * S);    // [N]
-  unsigned* skept = reinterpret_cast<unsigned*>(hist + N);  // [kRows] groups kept, then [4][kRows] experts chosen
-  float* swap = reinterpret_cast<float*>(skept + 4 * kRows);  // [swap_rows][kRows], what the halves tell one another
-  for (int e = threadIdx.x; e < N; e += 2 * kRows) {
+  constexpr int S = kTile + 1;  // odd: neither filling nor reading meets one bank
+  const int tid = threadIdx.x & (kTile - 1), half = threadIdx.x / kTile, lane = tid & 31, N = p.n;
+  double* exact = reinterpret_cast<double*>(smem4);  // [kTile / 32][N] of the warps that decide
+  float* sb = smem + kTile / 16 * N;                 // [N] bias, in whole float4s
+  float* tile = sb + (N + 3) / 4 * 4;                // [N][S]
+  int* hist = reinterpret_cast<int*>(tile + N * S);  // [N]
+  unsigned* skept = reinterpret_cast<unsigned*>(hist + N);  // [kTile] groups kept, then [4][kTile] experts chosen
+  float* swap = reinterpret_cast<float*>(skept + 4 * kTile);  // [swap_rows][kTile], what the halves tell one another
+  for (int e = threadIdx.x; e < N; e += 2 * kTile) {
     const float b = bias ? __ldg(bias + e) : 0.f;
     sb[e] = b >= -INFINITY ? b : -INFINITY;  // a NaN rules the expert out too
     hist[e] = 0;
@@ -485,18 +485,18 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
   const int size = N / p.groups, split = (size + 1) / 2;
   const int from = half ? split : 0, to = half ? size : split;  // this thread's part of a group
   const bool fours = size % 8 == 0;                             // both parts are whole fours
-  // a thread's float4s of a tile are 8 kRows values apart: so many rows and columns
+  // a thread's float4s of a tile are 8 kTile values apart: so many rows and columns
   const int fill_r = N == 1 ? 0 : (int)__umulhi(threadIdx.x * 4, magic), fill_c = threadIdx.x * 4 - fill_r * N;
-  const int step_c = 8 * kRows % N, step_at = step_c * S + 8 * kRows / N;
-  for (int64_t t0 = (int64_t)blockIdx.x * kRows; t0 < n; t0 += (int64_t)gridDim.x * kRows) {
-    const int rows = (int)min((int64_t)kRows, n - t0);
+  const int step_c = 8 * kTile % N, step_at = step_c * S + 8 * kTile / N;
+  for (int64_t t0 = (int64_t)blockIdx.x * kTile; t0 < n; t0 += (int64_t)gridDim.x * kTile) {
+    const int rows = (int)min((int64_t)kTile, n - t0);
     __syncthreads();  // the tile of the round before is read
     const float* src = logits + t0 * N;  // rows N values from a 16-byte border
     if (N % 4 == 0) {
       int c = fill_c;
       float* dst = tile + c * S + fill_r;
 #pragma unroll 4
-      for (int i = threadIdx.x * 4; i < rows * N; i += 8 * kRows) {
+      for (int i = threadIdx.x * 4; i < rows * N; i += 8 * kTile) {
         const float4 f = __ldg(reinterpret_cast<const float4*>(src + i));
         dst[0] = f.x;
         dst[S] = f.y;
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
       }
     } else {
 #pragma unroll 8
-      for (int i = threadIdx.x; i < rows * N; i += 2 * kRows) {
+      for (int i = threadIdx.x; i < rows * N; i += 2 * kTile) {
         const int r = N == 1 ? i : (int)__umulhi(i, magic);
         tile[(i - r * N) * S + r] = __ldg(src + i);
       }
@@ -527,27 +527,31 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
       const int e0 = half ? (N + 1) / 2 : 0, e1 = half ? N : (N + 1) / 2;
 #pragma unroll 8
       for (int e = e0; e < e1; ++e) top = fmaxf(top, there(col[e * S]) ? fminf(col[e * S], FLT_MAX) : -FLT_MAX);
-      swap[half * kRows + tid] = top;
+      swap[half * kTile + tid] = top;
       __syncthreads();
-      top = fmaxf(top, swap[(1 - half) * kRows + tid]);
+      top = fmaxf(top, swap[(1 - half) * kTile + tid]);
       float part[4] = {};
       for (int e = e0; e < e1; e += 4)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float l = e + j < e1 ? col[(e + j) * S] : -FLT_MAX;
-          part[j] += there(l) ? quick_exp(fminf(l, FLT_MAX) - top) : 0.f;
+          const float x = there(l) ? quick_exp(fminf(l, FLT_MAX) - top) : 0.f;
+          part[j] += x;
+          // from here on the tile holds these, -1 where the expert is out
+          if (!BY_LOGIT && e + j < e1) col[(e + j) * S] = there(l) ? x : -1.f;
         }
       total = (part[0] + part[1]) + (part[2] + part[3]);
       __syncthreads();
-      swap[half * kRows + tid] = total;
+      swap[half * kTile + tid] = total;
       __syncthreads();
-      total = swap[tid] + swap[kRows + tid];
+      total = swap[tid] + swap[kTile + tid];
       __syncthreads();
     }
     const float over = total > 0.f ? 1.f / total : 0.f;
-    auto score = [&](float l) {  // -1 where the expert is out
-      const float s = SIGMOID ? quick_sigmoid(l) : quick_exp(fminf(l, FLT_MAX) - top) * over;
-      return there(l) ? s : -1.f;
+    auto score = [&](float x) {  // from the tile; -1 where the expert is out
+      if (!SIGMOID) return x < 0.f ? -1.f : x * over;
+      const float s = quick_sigmoid(x);
+      return there(x) ? s : -1.f;
     };
     auto biased = [&](float s, float b) { return s < 0.f ? -INFINITY : s + b; };
     // what is compared, from the tile: logits, with groups (once they are scored) scores
@@ -592,9 +596,8 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
         float* c = col + g * size * S;
         const float* b = sb + g * size;
         auto look = [&](float* at, float bi) {
-          const float l = *at;
-          const float s = SIGMOID ? quick_sigmoid(l) : quick_exp(fminf(l, FLT_MAX) - top) * over;
-          const bool in = there(l);
+          const float x = *at, s = SIGMOID ? quick_sigmoid(x) : x * over;
+          const bool in = SIGMOID ? there(x) : x >= 0.f;
           const float v = in ? s + bi : -INFINITY;
           *at = in ? s : -1.f;  // from here on the tile holds the scores
           b2 = fmaxf(b2, fminf(b1, v));
@@ -613,7 +616,7 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
 #pragma unroll 1
           for (int i = 0; i < size; ++i, c += S, ++b) look(c, *b);
         }
-        swap[g * kRows + tid] = p.group_best == 2 && b2 > -INFINITY ? b1 + b2 : b1;
+        swap[g * kTile + tid] = p.group_best == 2 && b2 > -INFINITY ? b1 + b2 : b1;
       }
       __syncthreads();
       if (!half) {
@@ -624,7 +627,7 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
           int at = -1;
 #pragma unroll 4
           for (int g = 0; g < p.groups; ++g) {
-            const float x = swap[g * kRows + tid];
+            const float x = swap[g * kTile + tid];
             if (x > best) {
               best = x;
               at = g;
@@ -633,12 +636,12 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
           if (at >= 0) {
             kept |= 1u << at;
             last = best;
-            swap[at * kRows + tid] = -INFINITY;
+            swap[at * kTile + tid] = -INFINITY;
           }
         }
         float next = -INFINITY;
 #pragma unroll 4
-        for (int g = 0; g < p.groups; ++g) next = fmaxf(next, swap[g * kRows + tid]);
+        for (int g = 0; g < p.groups; ++g) next = fmaxf(next, swap[g * kTile + tid]);
         hard = next > -INFINITY && !(last - next > 2.f * wide + 2.4e-7f * (fabsf(last) + fabsf(next)));
         skept[tid] = kept;
       }
@@ -666,13 +669,13 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
     }
     if (half) {
 #pragma unroll
-      for (int j = 0; j <= K; ++j) swap[j * kRows + tid] = __int_as_float(key[j]);
+      for (int j = 0; j <= K; ++j) swap[j * kTile + tid] = __int_as_float(key[j]);
     }
     __syncthreads();
     if (!half) {
       int other[K + 1];
 #pragma unroll
-      for (int j = 0; j <= K; ++j) other[j] = __float_as_int(swap[j * kRows + tid]);
+      for (int j = 0; j <= K; ++j) other[j] = __float_as_int(swap[j * kTile + tid]);
       merge_keys(key, other, K + 1);
       // the values behind the keys, as they were compared
       float val[K + 1];
@@ -740,7 +743,7 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
         w[j] = idx[j] < 0 ? 0.f : col[idx[j] * S];
         most = idx[j] < 0 ? most : fmaxf(most, w[j]);
       }
-      if (p.groups > 1) {
+      if (p.groups > 1 || !(SIGMOID || BY_LOGIT)) {
         // scores near the smallest floats share out the scale in 64 bits
         hard |= p.renormalise && lastid >= 0 && most < 1e-30f;
       } else if (SIGMOID || (BY_LOGIT && p.sigmoid)) {
@@ -763,9 +766,9 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
 #pragma unroll
       for (int j = 0; j < K; ++j) sum += w[j];
       // a softmax's scores are divided by their sum already where groups were scored
-      const float f = p.renormalise                   ? (sum > 0.f ? p.scale / sum : 0.f)
+      const float f = p.renormalise               ? (sum > 0.f ? p.scale / sum : 0.f)
                       : p.sigmoid || p.groups > 1 ? p.scale
-                                                      : p.scale * over;
+                                                  : p.scale * over;
 #pragma unroll
       for (int j = 0; j < K; ++j) w[j] *= f;
       if (p.renormalise && idx[0] >= 0 && (K == 1 || idx[K > 1] < 0)) w[0] = p.scale;  // a single one: not by rounding
@@ -799,7 +802,7 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
         }
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        if (32 * q < N) skept[q * kRows + tid] = chosen[q];
+        if (32 * q < N) skept[q * kTile + tid] = chosen[q];
       __syncwarp();
       for (unsigned left = __ballot_sync(kAll, doubt); left; left &= left - 1) {
         const int from_lane = __ffs(left) - 1, r = (tid & ~31) + from_lane;
@@ -820,9 +823,9 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
               const float x = colr[e * S];
               v = BY_LOGIT ? (there(x) ? fminf(x, FLT_MAX) : -INFINITY)
                            : biased(p.groups > 1 ? x
-                                    : !there(x)  ? -1.f
-                                    : SIGMOID    ? quick_sigmoid(x)
-                                                 : quick_exp(fminf(x, FLT_MAX) - topr) * overr,
+                                    : !SIGMOID   ? (x < 0.f ? -1.f : x * overr)
+                                    : there(x)   ? quick_sigmoid(x)
+                                                 : -1.f,
                                     sb[e]);
             }
             const bool may = v > -INFINITY && !apart(lastr, v);
@@ -871,7 +874,7 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
           if (weights) weights[(t0 + r) * p.k + lane] = wj;
           if (id >= 0) {
             tile[id * S + r] = wj;
-            atomicOr(skept + (id >> 5) * kRows + r, 1u << (id & 31));
+            atomicOr(skept + (id >> 5) * kTile + r, 1u << (id & 31));
             if (counts) atomicAdd(hist + id, 1);
           }
         }
@@ -883,7 +886,7 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
         const int mid = (N / 2 + 7) / 8 * 8, e0 = half ? mid : 0, e1 = half ? N : min(mid, N);
         float* out = gates + t0 + e0 * ld;
         for (int e = e0; e < e1; e += 8) {  // eights do not cross a word of the mask
-          const unsigned bits = skept[(e >> 5) * kRows + tid] >> (e & 31);
+          const unsigned bits = skept[(e >> 5) * kTile + tid] >> (e & 31);
           const float* from_tile = col + e * S;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -897,7 +900,7 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
   }
   if (counts) {
     __syncthreads();
-    for (int e = threadIdx.x; e < N; e += 2 * kRows)
+    for (int e = threadIdx.x; e < N; e += 2 * kTile)
       if (hist[e]) atomicAdd(counts + e, hist[e]);
   }
 }
@@ -911,6 +914,7 @@ __global__ void __launch_bounds__(2 * kRows, 4) route_thread_kernel(
 // 35; 60,000 x 128: 37 / 30; 60,000 x 64: 12.5 / 12.9; 10,000 x 64: 5.9 / 7.2.  What is
 // left of the first is latency: its 132 MB pass at 3.8 TB/s.
 
+constexpr int kRows = 128;               // rows of a CTA's tile, at most
 constexpr int64_t kWholeRows = 1 << 22;  // values of an array
 
 template <int K>
@@ -1154,12 +1158,17 @@ template <int K>
 cudaError_t forward_threads(const RouteSpec& p, int64_t n, const float* logits, const float* bias, const RouteOut& o,
                             cudaStream_t s) {
   const int swap_rows = std::max(std::max(K + 1, 2), p.groups);
-  const size_t shared = sizeof(float) * ((size_t)(kRows + 1) * p.n + 10 * p.n + 4 + (size_t)(4 + swap_rows) * kRows);
-  const int64_t grid = std::min<int64_t>((n + kRows - 1) / kRows, kSms * 64);
+  const size_t shared = sizeof(float) * ((size_t)(kTile + 1) * p.n + (kTile / 16 + 2) * p.n + 4 + (size_t)(4 + swap_rows) * kTile);
+  // Short rows: the resident CTAs go on from tile to tile, since starting one (the biases,
+  // its counts into the whole) weighs beside a tile; long ones: a CTA a tile, so that
+  // those with rows to decide in 64 bits hold up no others.  Measured, going on / a
+  // CTA a tile, us: 300,000 x 8: 17.3 / 20.7; 400,000 x 16: 27 / 31; 500,000 x 32: 54 / 55;
+  // 172,050 x 48: 25.9 / 26.8; 300,000 x 64, k = 4: 85 / 76; 172,050 x 96: 110 / 90.
+  const int64_t grid = std::min<int64_t>((n + kTile - 1) / kTile, kSms * (p.n <= 32 ? 512 / kTile : 128));
   auto kernel = !bias && p.groups == 1 ? route_thread_kernel<K, false, true>
                 : p.sigmoid            ? route_thread_kernel<K, true, false>
                                        : route_thread_kernel<K, false, false>;
-  return launch_dependent(kernel, grid, 2 * kRows, shared, s, p, n, logits, bias, o.ids, o.weights, o.gates, o.ld,
+  return launch_dependent(kernel, grid, 2 * kTile, shared, s, p, n, logits, bias, o.ids, o.weights, o.gates, o.ld,
                           o.counts, divide_by(p.n));
 }
 
