@@ -183,6 +183,11 @@ def _new_on(stream, make):
         return make()
 
 
+def _new_f32(x, shape):
+    """A new array on x's device (without a dtype it is the cheaper call)."""
+    return x.new_empty(shape) if x.dtype is _types()["f32"] else x.new_empty(shape, dtype=_types()["f32"])
+
+
 def real_cg(l1: int, l2: int, l3: int) -> np.ndarray:
     C = np.zeros((2 * l1 + 1, 2 * l2 + 1, 2 * l3 + 1), dtype=np.float64)
     _check(_lib.cgtp_real_cg(l1, l2, l3, _np_ptr(C)))
@@ -530,7 +535,7 @@ class LayerNorm:
         h = ctypes.c_void_p()
         _check(_lib.cgtp_norm_create(irreps.encode(), float(eps), ctypes.byref(h)))
         self._h = h
-        self.irreps, self.eps = irreps, float(eps)
+        self.irreps, self.eps, self._ws_size = irreps, float(eps), (-1, 0)
         v = [ctypes.c_int64() for _ in range(3)]
         _check(_lib.cgtp_norm_info(h, *[ctypes.byref(t) for t in v]))
         self.d, self.n_weight, self.n_bias = (t.value for t in v)
@@ -546,14 +551,16 @@ class LayerNorm:
         except Exception:
             pass
 
-    def _new(self, x, shape):
-        return x.new_empty(shape) if x.dtype is _types()["f32"] else x.new_empty(shape, dtype=_types()["f32"])
-
     def _like(self, x, n):
         """A new [n, D] array for x (empty_like is the cheaper call)."""
         if x.dtype is _types()["f32"] and x.dim() == 2 and x.shape[1] == self.d:
             return _torch().empty_like(x)
-        return self._new(x, (n, self.d))
+        return _new_f32(x, (n, self.d))
+
+    def _like_weight(self, weight, x):
+        if weight is not None and weight.dtype is _types()["f32"] and weight.shape == (self.n_weight,):
+            return _torch().empty_like(weight)
+        return _new_f32(x, self.n_weight)
 
     def forward(self, x, weight=None, bias=None, out=None, stream=None):
         n, dev = x.shape[0], x.device
@@ -569,11 +576,13 @@ class LayerNorm:
         _check(_lib.cgtp_norm_workspace_size(self._h, n, ctypes.byref(b)))
         return b.value
 
-    def _ws(self, workspace, n, dev, stream):
+    def _ws(self, workspace, x, n, stream):
         if workspace is not None:
             return workspace
-        return _new_on(stream, lambda: _torch().empty(max(self.workspace_size(n), 256), dtype=_torch().uint8,
-                                                      device=dev))
+        size = self._ws_size  # of the last n: training asks for the same one again
+        if size[0] != n:
+            self._ws_size = size = n, max(self.workspace_size(n), 256) // 4
+        return _new_on(stream, lambda: x.new_empty(size[1]))
 
     def backward(self, x, weight, grad_out, want=("x", "weight", "bias"), grads=None, workspace=None,
                  stream=None):
@@ -581,13 +590,13 @@ class LayerNorm:
         n, dev = x.shape[0], x.device
         if grads is None:
             grads = _new_on(stream, lambda: (self._like(x, n) if "x" in want else None,
-                                             self._new(x, self.n_weight) if "weight" in want else None,
-                                             self._new(x, self.n_bias) if "bias" in want else None))
+                                             self._like_weight(weight, x) if "weight" in want else None,
+                                             _new_f32(x, self.n_bias) if "bias" in want else None))
         dx, dw, db = grads
         ptrs = _args(dev, (x, "x", n * self.d, "f32"), (weight, "weight", self.n_weight, "f32"),
                      (grad_out, "grad_out", n * self.d, "f32"), (dx, "grad_x", n * self.d, "f32"),
                      (dw, "grad_weight", self.n_weight, "f32"), (db, "grad_bias", self.n_bias, "f32"))
-        workspace = self._ws(workspace, n, dev, stream)  # held until the launch
+        workspace = self._ws(workspace, x, n, stream)  # held until the launch
         _check(_lib.cgtp_norm_backward(self._h, n, *ptrs, *_workspace(workspace, dev), _stream_of(dev, stream)))
         return dx, dw, db
 
@@ -600,14 +609,14 @@ class LayerNorm:
         if grads is None:
             grads = _new_on(stream, lambda: (self._like(x, n) if "g" in want else None,
                                              self._like(x, n) if "x" in want else None,
-                                             self._new(x, self.n_weight) if "weight" in want else None))
+                                             self._like_weight(weight, x) if "weight" in want else None))
         gg, gx, gw = grads
         ptrs = _args(dev, (x, "x", n * self.d, "f32"), (weight, "weight", self.n_weight, "f32"),
                      (grad_out, "grad_out", n * self.d, "f32"), (h_x, "h_x", n * self.d, "f32"),
                      (h_weight, "h_weight", self.n_weight, "f32"), (h_bias, "h_bias", self.n_bias, "f32"),
                      (gg, "grad_grad_out", n * self.d, "f32"), (gx, "grad_x", n * self.d, "f32"),
                      (gw, "grad_weight", self.n_weight, "f32"))
-        workspace = self._ws(workspace, n, dev, stream)  # held until the launch
+        workspace = self._ws(workspace, x, n, stream)  # held until the launch
         _check(_lib.cgtp_norm_double_backward(self._h, n, *ptrs, *_workspace(workspace, dev),
                                               _stream_of(dev, stream)))
         return gg, gx, gw
@@ -660,13 +669,13 @@ class Router:
         return t.data_ptr(), ld
 
     def _outs(self, logits, n, want):
-        f32, i32 = _types()["f32"], _types()["i32"]
-        e = lambda dtype, *shape: logits.new_empty(shape, dtype=dtype)
-        gates = e(f32, self.n_experts, -(-n // 4) * 4) if "gates" in want else None
+        i32, new = _types()["i32"], logits.new_empty
+        ids = new((n, self.k), dtype=i32) if "ids" in want else None
+        weights = _new_f32(logits, (n, self.k)) if "weights" in want else None
+        gates = _new_f32(logits, (self.n_experts, -(-n // 4) * 4)) if "gates" in want else None
         if gates is not None and n % 4:
             gates = gates[:, :n]
-        return (e(i32, n, self.k) if "ids" in want else None, e(f32, n, self.k) if "weights" in want else None,
-                gates, e(i32, self.n_experts) if "counts" in want else None)
+        return ids, weights, gates, new(self.n_experts, dtype=i32) if "counts" in want else None
 
     def forward(self, logits, bias=None, want=("ids", "weights", "gates", "counts"), outs=None, stream=None):
         """(ids [n, k] int32, weights [n, k], gates [n_experts, n], counts
@@ -689,7 +698,7 @@ class Router:
         grad_gates [n_experts, n] (rows may be padded)."""
         n, dev = logits.shape[0], logits.device
         if grad_logits is None:
-            grad_logits = _new_on(stream, lambda: logits.new_empty((n, self.n_experts), dtype=_types()["f32"]))
+            grad_logits = _new_on(stream, lambda: _new_f32(logits, (n, self.n_experts)))
         pl, pi, pw, po = _args(dev, (logits, "logits", n * self.n_experts, "f32"), (ids, "ids", n * self.k, "i32"),
                                (grad_weights, "grad_weights", n * self.k, "f32"),
                                (grad_logits, "grad_logits", n * self.n_experts, "f32"))
