@@ -557,11 +557,6 @@ class LayerNorm:
             return _torch().empty_like(x)
         return _new_f32(x, (n, self.d))
 
-    def _like_weight(self, weight, x):
-        if weight is not None and weight.dtype is _types()["f32"] and weight.shape == (self.n_weight,):
-            return _torch().empty_like(weight)
-        return _new_f32(x, self.n_weight)
-
     def forward(self, x, weight=None, bias=None, out=None, stream=None):
         n, dev = x.shape[0], x.device
         if out is None:
@@ -590,7 +585,7 @@ class LayerNorm:
         n, dev = x.shape[0], x.device
         if grads is None:
             grads = _new_on(stream, lambda: (self._like(x, n) if "x" in want else None,
-                                             self._like_weight(weight, x) if "weight" in want else None,
+                                             _new_f32(x, self.n_weight) if "weight" in want else None,
                                              _new_f32(x, self.n_bias) if "bias" in want else None))
         dx, dw, db = grads
         ptrs = _args(dev, (x, "x", n * self.d, "f32"), (weight, "weight", self.n_weight, "f32"),
@@ -609,7 +604,7 @@ class LayerNorm:
         if grads is None:
             grads = _new_on(stream, lambda: (self._like(x, n) if "g" in want else None,
                                              self._like(x, n) if "x" in want else None,
-                                             self._like_weight(weight, x) if "weight" in want else None))
+                                             _new_f32(x, self.n_weight) if "weight" in want else None))
         gg, gx, gw = grads
         ptrs = _args(dev, (x, "x", n * self.d, "f32"), (weight, "weight", self.n_weight, "f32"),
                      (grad_out, "grad_out", n * self.d, "f32"), (h_x, "h_x", n * self.d, "f32"),
