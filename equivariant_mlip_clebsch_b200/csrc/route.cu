@@ -736,16 +736,28 @@ __global__ void __launch_bounds__(2 * kTile, 512 / kTile) route_thread_kernel(
         }
       }
       // weights of the chosen, in order: from the scores where the tile holds them
-      float w[K], sum = 0.f, most = -FLT_MAX;
+      const bool scored = p.groups > 1 || !(SIGMOID || BY_LOGIT);
+      float w[K], sum = 0.f, most = -FLT_MAX, least = 1.f;
 #pragma unroll
       for (int j = 0; j < K; ++j) {
         if (j >= p.k || !(val[j] > -INFINITY)) idx[j] = -1;
         w[j] = idx[j] < 0 ? 0.f : col[idx[j] * S];
         most = idx[j] < 0 ? most : fmaxf(most, w[j]);
+        least = idx[j] < 0 ? least : fminf(least, w[j]);
       }
-      if (p.groups > 1 || !(SIGMOID || BY_LOGIT)) {
-        // scores near the smallest floats share out the scale in 64 bits
-        hard |= p.renormalise && lastid >= 0 && most < 1e-30f;
+      // Small scores are formed again from their logits: the quick exponential of x is off
+      // by |x| 2^-23 of itself, and gives 0 below the smallest normal float.
+      const bool again = scored && lastid >= 0 && least < 1e-13f;
+      if (again) {
+        most = -FLT_MAX;
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+          w[j] = idx[j] < 0 ? 0.f : __ldg(row + idx[j]);
+          most = idx[j] < 0 ? most : fmaxf(most, w[j]);
+        }
+      }
+      if (scored && !again) {
+        // the scores stand in w
       } else if (SIGMOID || (BY_LOGIT && p.sigmoid)) {
         most = p.renormalise ? fminf(most, 0.f) : 0.f;
 #pragma unroll
@@ -766,9 +778,9 @@ __global__ void __launch_bounds__(2 * kTile, 512 / kTile) route_thread_kernel(
 #pragma unroll
       for (int j = 0; j < K; ++j) sum += w[j];
       // a softmax's scores are divided by their sum already where groups were scored
-      const float f = p.renormalise               ? (sum > 0.f ? p.scale / sum : 0.f)
-                      : p.sigmoid || p.groups > 1 ? p.scale
-                                                  : p.scale * over;
+      const float f = p.renormalise                           ? (sum > 0.f ? p.scale / sum : 0.f)
+                      : p.sigmoid || (p.groups > 1 && !again) ? p.scale
+                                                              : p.scale * over;
 #pragma unroll
       for (int j = 0; j < K; ++j) w[j] *= f;
       if (p.renormalise && idx[0] >= 0 && (K == 1 || idx[K > 1] < 0)) w[0] = p.scale;  // a single one: not by rounding

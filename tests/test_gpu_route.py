@@ -370,3 +370,47 @@ def test_backward_ignores_the_gradient_of_what_is_out(dev):
             d = r.backward(T(l, dev), T(ids, dev), T(gw, dev)).cpu().numpy()
             ref = O.route_backward(l, ids, clean, None, score, renormalise)
             assert np.abs(d - ref).max() < 1e-6
+
+
+@pytest.mark.parametrize("E,kw", [(64, dict(k=8)), (64, dict(k=8, renormalise=False)), (16, dict(k=4)), (40, dict(k=5, n_groups=4, top_groups=2)),
+                                  (40, dict(k=5, n_groups=4, top_groups=2, renormalise=False)), (24, dict(k=8, score="sigmoid")),
+                                  (64, dict(k=8, score="sigmoid", n_groups=8, top_groups=4)), (128, dict(k=8, scale=3.0))])
+def test_weights_of_small_scores(E, kw, dev):
+    """Logits far apart, and a bias that steers to the small scores (some below
+    the smallest float): each weight within the bound of its own size, on the
+    form for few rows and on the one for many."""
+    rng = np.random.default_rng(21)
+    base = (rng.choice([1.0, 20.0, 45.0], size=(200, 1)) * rng.standard_normal((200, E))).astype(np.float32)
+    base[::3] -= 40
+    bias = np.where(rng.random(E) < 0.5, 2.0, -2.0).astype(np.float32) + (0.1 * rng.standard_normal(E)).astype(np.float32)
+    oi, ow, _, _, _ = O.route_forward(base, bias, **kw)
+    for pick in (np.arange(200), rng.integers(0, 200, size=20001)):
+        ids, w, _, _ = C().Router(E, **kw).forward(T(base[pick], dev), T(bias, dev))
+        assert np.array_equal(ids.cpu().numpy(), oi[pick])
+        assert np.all(np.abs(w.cpu().numpy() - ow[pick]) <= 160 * U * ow[pick] + kw.get("scale", 1.0) * 1.2e-38)
+
+
+@pytest.mark.parametrize("E,kw", [(4, dict(k=1, renormalise=False)), (16, dict(k=2)), (32, dict(k=4, score="sigmoid")),
+                                  (12, dict(k=4, n_groups=12, top_groups=5))])
+@pytest.mark.parametrize("bias", [False, True])
+def test_route_more_rows_than_a_wave(E, kw, bias, dev):
+    """Short rows, so many that a CTA takes several tiles: as the same rows in
+    parts that it takes at once."""
+    n, part = 300_001, 60_000
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(5)
+    l = torch.randn(n, E, device=dev, generator=gen)
+    l[torch.rand(n, E, device=dev, generator=gen) < 0.1] = LOW
+    b = 0.1 * torch.randn(E, device=dev, generator=gen) if bias else None
+    r = C().Router(E, **kw)
+    ids, w, gates, counts = r.forward(l, b)
+    total = torch.zeros(E, dtype=torch.int32, device=dev)
+    for t in range(0, n, part):
+        i, v, g, c = r.forward(l[t:t + part].clone(), b)
+        assert torch.equal(ids[t:t + part], i)
+        # the last part, one row, is decided by the form for few rows: each form's weights are
+        # within 160 u of the exact ones, so within 320 u of the other's; else the same bits
+        u = 320 * U if len(i) < part else 0.0
+        assert ((w[t:t + part] - v).abs() <= u * v).all() and ((gates[:, t:t + part] - g).abs() <= u * g).all()
+        total += c
+    assert torch.equal(counts, total)
