@@ -249,7 +249,7 @@ __device__ __forceinline__ bool route_row_fast(const RouteSpec& p, const float* 
     v[q] = none;
     if (there(l[q])) {
       const float b = bias ? __ldg(bias + q * 32 + lane) : 0.f;
-      const float x = by_logit ? l[q] : s[q] * over + b;
+      const float x = by_logit ? l[q] + 0.f : s[q] * over + b;  // + 0: -0 and 0 are one value, and so one integer
       if (x > -INFINITY) v[q] = ordered(x);
     }
   }
@@ -314,7 +314,7 @@ __device__ __forceinline__ bool route_row_fast(const RouteSpec& p, const float* 
       if (e < p.n && !(kept >> (e / size) & 1)) v[q] = none;
     }
   }
-  // equal logits and biases: in their right order already
+  // equal logits and biases are equal values here, of which take() gives the lowest index first
   auto same = [&](int a, int b) {
     return __ldg(row + a) == __ldg(row + b) && (!bias || __ldg(bias + a) == __ldg(bias + b));
   };

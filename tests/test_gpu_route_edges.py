@@ -1,0 +1,73 @@
+"""GPU parity of the router where its forms could part from the definition:
+zeros of both signs, biases of the lowest float, saturated sigmoids, and
+gradients of a row whose weight lies almost all on one expert.
+
+Choices are equal to the FP64 oracle's.  A weight is off by at most 160 u of
+itself (the parity tests count its roundings).  The gradients' bound: with
+the shares p of a row and any constant c, sum p d is c + sum p (d - c), so a
+logit's gradient is
+  w (d - c - sum p (d - c))
+whatever c; with c the d of an expert that holds more than half of the row it
+has no terms that cancel as a whole.  Shares are off by 160 u of themselves, the
+differences and the sum of at most 64 terms by less than that again: 320 u of
+w (|d - c| + sum p |d - c|), and (1 - p) of a sigmoid, formed from its logit,
+is inside that too.
+"""
+import numpy as np
+import pytest
+
+import oracle as O
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+U = 2.0 ** -24
+LOW = float(np.finfo(np.float32).min)
+
+
+def C():
+    from equivariant_mlip_clebsch_b200 import cgtp
+    return cgtp
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available()
+    return torch.device("cuda:0")
+
+
+def T(a, dev):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(dev)
+
+
+def choices(l, bias, kw, dev, n):
+    """The kernel's ids, weights, gates and counts of n rows drawn in turn from
+    l's against the oracle's."""
+    pick = np.arange(n) % len(l)
+    oi, ow, _, _, _ = O.route_forward(l, bias, **kw)
+    E = l.shape[1]
+    ids, w, gates, counts = C().Router(E, **kw).forward(T(l[pick], dev), None if bias is None else T(bias, dev))
+    assert np.array_equal(ids.cpu().numpy(), oi[pick])
+    assert np.all(np.abs(w.cpu().numpy() - ow[pick]) <= 160 * U * ow[pick] + kw.get("scale", 1.0) * 1.2e-38)
+    assert np.array_equal(counts.cpu().numpy(), np.bincount(oi[pick][oi[pick] >= 0], minlength=E))
+    ref = np.zeros((E + 1, n), np.float32)
+    ref[np.where(oi[pick] < 0, E, oi[pick]), np.arange(n)[:, None]] = w.cpu().numpy()
+    assert np.array_equal(gates.cpu().numpy(), ref[:E])
+
+
+@pytest.mark.parametrize("n", [60, 20001])
+@pytest.mark.parametrize("E,kw", [(4, dict(k=1)), (4, dict(k=2, renormalise=False)), (24, dict(k=3, score="sigmoid")),
+                                  (64, dict(k=8)), (64, dict(k=12)), (75, dict(k=5, score="sigmoid", renormalise=False)),
+                                  (200, dict(k=4, renormalise=False))])
+def test_zeros_of_both_signs_are_equal(E, kw, n, dev):
+    """Logits times a mask of zeros and ones: -0.0 and 0.0 are one value, and the
+    lowest index goes first, also across the cut of the k best."""
+    rng = np.random.default_rng(31)
+    l = rng.standard_normal((60, E)).astype(np.float32)
+    l *= rng.random((60, E)) < np.linspace(0, 0.6, 60)[:, None]  # a negative logit's zero is -0.0
+    l[0, :4] = [-0.0, 0.0, -1.0, 0.0]
+    l[0, 4:] = -1.0
+    l[1] = np.where(np.arange(E) % 2 == 0, -0.0, 0.0)
+    assert np.signbit(l[l == 0]).any() and not np.signbit(l[l == 0]).all()
+    choices(l, None, kw, dev, n)
+    choices(l, np.where(np.arange(E) % 3 == 0, -0.0, 0.0).astype(np.float32), kw, dev, n)
