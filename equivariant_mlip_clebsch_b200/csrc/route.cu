@@ -200,6 +200,11 @@ __device__ __forceinline__ float value_error(int n, bool sigmoid) {
   return sigmoid ? 4e-7f : 6e-7f + (float)(n / 8 + 4) * 6e-8f;
 }
 
+// The score of a group of two available values.  Biases of the lowest float leave
+// their sum available, but below what FP32 holds; as the lowest float it is close to
+// any other such group, and 64 bits decide between them.
+__device__ __forceinline__ float pair_score(float b1, float b2) { return fmaxf(b1 + b2, -FLT_MAX); }
+
 // The weight of a warp's row: lane j has the j-th choice (-1: none) and its
 // logit; the row's largest logit and one over its softmax's sum.
 __device__ __forceinline__ float row_weight(const RouteSpec& p, int id, float l, float top, float over) {
@@ -291,7 +296,7 @@ __device__ __forceinline__ bool route_row_fast(const RouteSpec& p, const float* 
       float sum = b1;
       if (p.group_best == 2) {
         const float b2 = unordered(__reduce_max_sync(kAll, m));
-        if (b2 > -INFINITY) sum += b2;
+        if (b2 > -INFINITY) sum = pair_score(b1, b2);
       }
       if (lane == g) mine = sum;
     }
@@ -616,7 +621,7 @@ __global__ void __launch_bounds__(2 * kTile, 512 / kTile) route_thread_kernel(
 #pragma unroll 1
           for (int i = 0; i < size; ++i, c += S, ++b) look(c, *b);
         }
-        swap[g * kTile + tid] = p.group_best == 2 && b2 > -INFINITY ? b1 + b2 : b1;
+        swap[g * kTile + tid] = p.group_best == 2 && b2 > -INFINITY ? pair_score(b1, b2) : b1;
       }
       __syncthreads();
       if (!half) {

@@ -71,3 +71,19 @@ def test_zeros_of_both_signs_are_equal(E, kw, n, dev):
     assert np.signbit(l[l == 0]).any() and not np.signbit(l[l == 0]).all()
     choices(l, None, kw, dev, n)
     choices(l, np.where(np.arange(E) % 3 == 0, -0.0, 0.0).astype(np.float32), kw, dev, n)
+
+
+@pytest.mark.parametrize("n", [60, 20001])
+@pytest.mark.parametrize("kw", [dict(k=8, score="sigmoid"), dict(k=8, renormalise=False), dict(k=12)])
+def test_biases_of_the_lowest_float(kw, n, dev):
+    """A bias of the lowest float puts an expert last, it does not rule it out: a
+    group of two such experts, whose sum is below the lowest float, can be chosen."""
+    rng = np.random.default_rng(32)
+    kw = dict(kw, n_groups=8, top_groups=4)
+    l = rng.standard_normal((60, 32)).astype(np.float32)
+    for open_experts in ([0, 2], [13, 14, 30], [], list(range(24))):
+        bias = np.full(32, LOW, np.float32)
+        bias[open_experts] = 0.1 * rng.standard_normal(len(open_experts))
+        choices(l, bias, kw, dev, n)
+        bias[1::4] = -np.inf  # one of every group out
+        choices(l, bias, kw, dev, n)
