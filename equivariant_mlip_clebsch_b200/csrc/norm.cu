@@ -306,20 +306,23 @@ __device__ __forceinline__ void norm_rows(const NormSeg& s, int o, int D, float 
     const float r = rsqrtf(fmaf(t[0], inv, eps));
     // From here on by xc = xh / r: what projects on xh is sum(z xc) xc / (sum(xc^2) + N
     // eps), without the rounding of r twice.
-    float along = 0.f, shift = 0.f, ph = 0.f, rb = 0.f, rl = 0.f;
+    float along = 0.f, shift = 0.f, ph = 0.f, rb = 0.f, rl = 0.f, rc = 0.f;
     if constexpr (OP != kForward) {
       const float over = 1.f / fmaf((float)len, eps, t[0]);
       if constexpr (OP == kBackward) {  // grad_x = r (a - mean(a)) - r (sum(a xc) over) xc
         along = -r * (t[1] * over);
         shift = -r * ma;
       }
-      if constexpr (OP == kDouble) {  // gx = r^2 (cx xh - be P a - al P h) + r (P k - de xh)
+      // gx = r (r (cx xh - be P a - al P h) + P k - de xh): only xh = r xc meets r once
+      // more before the sum, since r^2 and r^3 leave FP32 where eps is small
+      if constexpr (OP == kDouble) {
         const float al = t[1] * inv * r, be = t[2] * inv * r, ga = t[4] * inv;
         ph = -(t[2] * over);
-        along = r * (r * r * (3.f * al * be - ga) - t[3] * over);
-        rb = -r * r * be;
-        rl = -r * r * al;
-        shift = -(rb * ma + r * mk);
+        along = -(t[3] * over);
+        rc = r * (3.f * al * be - ga);
+        rb = -r * be;
+        rl = -r * al;
+        shift = -(rb * ma + mk);
       }
     }
 #pragma unroll
@@ -359,9 +362,9 @@ __device__ __forceinline__ void norm_rows(const NormSeg& s, int o, int D, float 
             const int e = 4 * q + j;
             const float xh = x[e] * r, jh = r * fmaf(ph, x[e], h[e]);
             y[j] = fmaf(w[j], jh, CENTRED ? fmaf(k[j], xh, b[j]) : k[j] * xh);
-            const float c = fmaf(rb, w[j], r * k[j]);  // of g
-            const float lin = fmaf(rl, h[e], x[e] * along);
-            z[j] = fmaf(c, g[e], CENTRED ? lin + shift : lin);
+            const float c = fmaf(rb, w[j], k[j]);  // of g
+            const float lin = fmaf(rl, h[e], fmaf(x[e], along, CENTRED ? fmaf(xh, rc, shift) : xh * rc));
+            z[j] = r * fmaf(c, g[e], lin);
             p[j] = g[e] * jh;
           }
           if (a.out) store4<SHIFT>(a.out + at + 4 * q * W, whole, some, y);
