@@ -309,8 +309,8 @@ __device__ __forceinline__ void norm_rows(const NormSeg& s, int o, int D, float 
     float along = 0.f, shift = 0.f, ph = 0.f, rb = 0.f, rl = 0.f, rc = 0.f;
     if constexpr (OP != kForward) {
       const float over = 1.f / fmaf((float)len, eps, t[0]);
-      if constexpr (OP == kBackward) {  // grad_x = r (a - mean(a)) - r (sum(a xc) over) xc
-        along = -r * (t[1] * over);
+      if constexpr (OP == kBackward) {  // grad_x = r (a - mean(a)) - (sum(a xc) over) xh; r^2 a may leave FP32
+        along = -(t[1] * over);
         shift = -r * ma;
       }
       // gx = r (r (cx xh - be P a - al P h) + P k - de xh): only xh = r xc meets r once
@@ -346,9 +346,10 @@ __device__ __forceinline__ void norm_rows(const NormSeg& s, int o, int D, float 
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int e = 4 * q + j;
+            const float xh = x[e] * r;
             gq[j] = g[e];
-            p[j] = g[e] * (x[e] * r);
-            y[j] = fmaf(x[e], along, CENTRED ? fmaf(g[e] * w[j], r, shift) : g[e] * w[j] * r);
+            p[j] = g[e] * xh;
+            y[j] = fmaf(xh, along, CENTRED ? fmaf(g[e] * w[j], r, shift) : g[e] * w[j] * r);
           }
           if (a.out) store4<SHIFT>(a.out + at + 4 * q * W, whole, some, y);
           if (dw) add_to(acc[q * T], make_float4(p[0], p[1], p[2], p[3]));

@@ -58,3 +58,16 @@ def test_second_order_of_zero_rows(dev):
     assert not gx.any() and not gg[:, :8].any() and not gw[:8].any()
     assert (gg[:, 8:] * eps ** 0.5 - 1).abs().max().item() <= 8 * 2.0 ** -24
     assert (gw[8:] * eps ** 0.5 - 9).abs().max().item() <= 9 * 16 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("eps", EPS)
+@pytest.mark.parametrize("irreps", IRREPS)
+def test_backward_of_small_rows(irreps, eps, dev, monkeypatch):
+    monkeypatch.setattr(N, "EPS", eps)
+    v, d = small(irreps, eps, 42)
+    mag = magnitudes(irreps, v, 14)
+    dx, dw, db = C().LayerNorm(irreps, eps).backward(d["x"], d["w"], d["g"])
+    rx, rw, rb = O.norm_backward(irreps, v["x"], v["w"], v["g"], eps)
+    close(dx, rx, mag["dx"], K, "grad_x")
+    close(dw, rw, mag["dw"], K + 700, "grad_weight")
+    close(db, rb, mag["db"], K + 700, "grad_bias")
