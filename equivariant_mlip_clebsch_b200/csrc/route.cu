@@ -1013,7 +1013,7 @@ __global__ void __launch_bounds__(2 * kRows, K <= 8 ? 5 : 2) route_chosen_backwa
         }
         l[j] = fminf(l[j], FLT_MAX);
       }
-      float m = 0.f, sum = 0.f, dot = 0.f;
+      float m = 0.f, sum = 0.f, dot = 0.f, ref = 0.f;
       if (p.renormalise) {
         m = -FLT_MAX;
 #pragma unroll
@@ -1035,19 +1035,30 @@ __global__ void __launch_bounds__(2 * kRows, K <= 8 ? 5 : 2) route_chosen_backwa
           sum += share[j];
         }
       }
+      // Renormalised, d_j - sum(share d): where one share is nearly 1 its d and the sum
+      // cancel.  So by differences: pair by pair, or for many places from the d of a share
+      // above a half, d_j - ref - sum(share (d - ref)).
       if (p.renormalise) {
 #pragma unroll
         for (int j = 0; j < K; ++j)
           if (id[j] >= 0) {
             share[j] /= sum;
-            dot = fmaf(d[j], share[j], dot);
+            if (K > 8 && share[j] > 0.5f) ref = d[j];
           }
+        if (K > 8) {
+#pragma unroll
+          for (int j = 0; j < K; ++j)
+            if (id[j] >= 0) {
+              d[j] -= ref;
+              dot = fmaf(d[j], share[j], dot);
+            }
+        }
       }
 #pragma unroll
       for (int j = 0; j < K; ++j)
         if (id[j] >= 0) {
           float x = d[j] - dot;
-          if (K <= 8 && p.renormalise) {  // pair by pair: where one share is nearly 1 its d and dot cancel
+          if (K <= 8 && p.renormalise) {
             x = 0.f;
 #pragma unroll
             for (int i = 0; i < K; ++i) x = fmaf(share[i], d[j] - d[i], x);

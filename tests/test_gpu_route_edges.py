@@ -87,3 +87,46 @@ def test_biases_of_the_lowest_float(kw, n, dev):
         choices(l, bias, kw, dev, n)
         bias[1::4] = -np.inf  # one of every group out
         choices(l, bias, kw, dev, n)
+
+
+def shifted(l, ids, d, kw):
+    """The gradient's magnitudes [rows, E] by the module's bound, for d [rows, k]."""
+    n, E = l.shape
+    scale, renormalise, sigmoid = kw.get("scale", 1.0), kw.get("renormalise", True), kw.get("score") == "sigmoid"
+    z = l.astype(np.float64)
+    p = np.exp(z - z.max(1, keepdims=True))
+    p = 1 / (1 + np.exp(-z)) if sigmoid else p / p.sum(1, keepdims=True)
+    de, chosen = np.zeros((n, E)), np.zeros((n, E), bool)
+    np.put_along_axis(de, ids, d.astype(np.float64), 1)
+    np.put_along_axis(chosen, ids, True, 1)
+    share = np.where(chosen, p, 0) if renormalise else p
+    share = share / share.sum(1, keepdims=True)
+    top = share.argmax(1)[:, None]
+    c = np.where(np.take_along_axis(share, top, 1) > 0.5, np.take_along_axis(de, top, 1), 0.0)
+    mag = scale * share * (np.abs(de - c) + (share * np.abs(de - c)).sum(1, keepdims=True))
+    return mag * (1 - p) if sigmoid else mag
+
+
+def dominant(n, E, seed):
+    """Rows with one logit some 3 to 15 above the others."""
+    rng = np.random.default_rng(seed)
+    l = rng.standard_normal((n, E)).astype(np.float32)
+    l[np.arange(n), rng.integers(0, E, n)] += np.linspace(3, 15, n, dtype=np.float32)
+    return rng, l
+
+
+@pytest.mark.parametrize("E,kw", [(64, dict(k=12)), (40, dict(k=32, scale=2.5)), (200, dict(k=9)), (64, dict(k=8)), (5, dict(k=2)),
+                                  (64, dict(k=12, score="sigmoid"))])
+def test_gradient_of_a_dominant_share(E, kw, dev):
+    """Renormalised: next to a share of 1 - 1e-6 each gradient is right to its own
+    size, not to that of the d it is formed from."""
+    rng, l = dominant(200, E, 33)
+    if kw.get("score") == "sigmoid":  # shares of e^(l - largest) / (1 + e^l)
+        l -= 12
+    r = C().Router(E, **kw)
+    ids = r.forward(T(l, dev))[0].cpu().numpy()
+    d = (1 + 0.1 * rng.standard_normal(ids.shape)).astype(np.float32)
+    got = r.backward(T(l, dev), T(ids, dev), T(d, dev)).cpu().numpy().astype(np.float64)
+    ref = O.route_backward(l, ids, d, None, **{k: v for k, v in kw.items() if k in ("score", "renormalise", "scale")})
+    mag = shifted(l, ids, d, kw)
+    assert (np.abs(got - ref) <= 320 * U * mag + 1e-37).all(), float((np.abs(got - ref) / (U * mag + 1e-37)).max())
