@@ -495,7 +495,7 @@ def route_forward(logits, bias, k: int, score="softmax", n_groups=1, top_groups=
             tot = sum(z.values())
             s = {e: z[e] / tot for e in on}
         else:
-                s = {e: 1.0 / (1.0 + np.exp(-max(l[e], -700.0))) for e in on}
+            s = {e: 1.0 / (1.0 + np.exp(-max(l[e], -700.0))) for e in on}
         for e in on:
             S[t, e] = s[e]
         v = {e: s[e] + b[e] for e in on if s[e] + b[e] > -np.inf}
@@ -534,6 +534,7 @@ def route_backward(logits, ids, grad_weights, grad_gates, score="softmax", renor
     """grad_logits [rows, n_experts] with the choice held fixed: the Jacobian
     of the weights with respect to the scores, then of the scores."""
     logits = _f64(logits)
+    grad_weights, grad_gates = (None if g is None else _f64(g) for g in (grad_weights, grad_gates))
     n, E = logits.shape
     k = ids.shape[1]
     out = np.zeros((n, E))
