@@ -130,3 +130,37 @@ def test_gradient_of_a_dominant_share(E, kw, dev):
     ref = O.route_backward(l, ids, d, None, **{k: v for k, v in kw.items() if k in ("score", "renormalise", "scale")})
     mag = shifted(l, ids, d, kw)
     assert (np.abs(got - ref) <= 320 * U * mag + 1e-37).all(), float((np.abs(got - ref) / (U * mag + 1e-37)).max())
+
+
+@pytest.mark.parametrize("E,k", [(3, 2), (8, 1), (16, 2), (30, 5), (64, 8), (100, 3), (200, 32), (512, 4)])
+def test_gradient_of_a_dominant_score(E, k, dev):
+    """The plain softmax, where the dominant expert is among the chosen (the first
+    of them) and where it is not."""
+    rng, l = dominant(200, E, 34)
+    kw = dict(k=k, renormalise=False, scale=1.5)
+    r = C().Router(E, **kw)
+    first = r.forward(T(l, dev))[0].cpu().numpy()
+    other = np.argsort(l, 1)[:, :k].astype(np.int32)
+    for ids in (first, other):
+        d = (1 + 0.1 * rng.standard_normal(ids.shape)).astype(np.float32)
+        got = r.backward(T(l, dev), T(ids, dev), T(d, dev)).cpu().numpy().astype(np.float64)
+        ref = O.route_backward(l, ids, d, None, renormalise=False, scale=1.5)
+        mag = shifted(l, ids, d, kw)
+        assert (np.abs(got - ref) <= 320 * U * mag + 1e-37).all(), float((np.abs(got - ref) / (U * mag + 1e-37)).max())
+
+
+def test_dominant_score_listed_twice(dev):
+    """Each place of a repeated id counts, also of the dominant one's."""
+    rng, l = dominant(200, 16, 35)
+    top = l.argmax(1)
+    ids = np.stack([top, top, (top + 1) % 16, top], 1).astype(np.int32)
+    d = rng.standard_normal(ids.shape).astype(np.float32)
+    r = C().Router(16, 4, renormalise=False)
+    got = r.backward(T(l, dev), T(ids, dev), T(d, dev)).cpu().numpy().astype(np.float64)
+    ref = O.route_backward(l, ids, d, None, renormalise=False)
+    # as one place with the sum of the three, itself off by 2 u of the sum of magnitudes
+    mag = shifted(l, ids[:, 1:3], np.stack([d[:, [0, 1, 3]].sum(1), d[:, 2]], 1), dict(renormalise=False))
+    p = np.exp(l - l.max(1, keepdims=True).astype(np.float64))
+    p /= p.sum(1, keepdims=True)
+    mag += 2 / 320 * np.abs(d).sum(1, keepdims=True) * p * np.where(np.arange(16) == top[:, None], 1 - p, 1)
+    assert (np.abs(got - ref) <= 320 * U * mag + 1e-37).all(), float((np.abs(got - ref) / (U * mag + 1e-37)).max())
