@@ -353,8 +353,10 @@ cgtp_status cgtp_sparse_backward(cgtp_plan plan, int64_t n_recv, int64_t n_send,
  *   weight [n_weight]  one per channel, blocks in order (NULL: ones)
  *   bias   [n_bias]    one per 0e channel, blocks in order (NULL: zeros)
  * Statistics and sums are FP32; a row's statistics are formed again from x in
- * the backward calls, nothing is kept from the forward.  A NaN or infinity in
- * x reaches only its own block of its own row (and the weight gradients).
+ * the backward calls, nothing is kept from the forward.  The sum of a block's
+ * xc^2 has to be an FP32 number (below 3.4e38: values up to some 1e18); of
+ * larger values r and xh are 0.  A NaN or infinity in x reaches only its own
+ * block of its own row (and the weight gradients).
  * Outputs are overwritten and must not alias inputs.  All results are bitwise
  * reproducible (no atomics).
  *
@@ -417,11 +419,13 @@ cgtp_status cgtp_norm_double_backward(cgtp_norm norm, int64_t n, const float* x,
  * has a logit per expert and is given to its k best ones.  Where the BranchIP
  * page's router gives an edge one gate, this gives it one per expert; row e
  * of gates is the gate array of cgtp_sparse_forward for expert e.
- *   s = softmax(logits) or sigmoid(logits), over the row's available experts
- *   v = s + bias                    (bias only steers the choice)
- *   an expert is available to a row when its logit is above the lowest
- *   float (so neither NaN nor -inf) and v is above -inf and not NaN; an
- *   infinite logit counts as the largest float
+ *   s = softmax(logits) or sigmoid(logits), over the experts whose logit is
+ *   above the lowest float (so neither NaN nor -inf); an infinite logit
+ *   counts as the largest float
+ *   v = s + bias                    (bias only steers the choice: an expert
+ *   that a bias of -inf or NaN rules out still counts in a softmax's sum)
+ *   an expert is available to a row when it has a score and v is above -inf
+ *   and not NaN (a bias of the lowest float puts it last, not out)
  *   groups: n_groups equal ranges of experts, each scored by the sum of its
  *   group_best (1 or 2) best available v; only the top_groups best stay
  *   ids: the k best available experts left, by v, best first
@@ -431,6 +435,10 @@ cgtp_status cgtp_norm_double_backward(cgtp_norm norm, int64_t n, const float* x,
  * logits, whose order is the scores'.  Of equal values the lowest index wins.
  * Where fewer than k experts are left, the remaining ids are -1 with weight
  * 0; a row with none left has all gates 0.
+ * A gate jumps between 0 and its weight where the choice changes (with k =
+ * n_experts there is no choice).  An energy whose logits depend on positions
+ * is therefore not continuous there, other than with a gate that goes to 0
+ * smoothly; and, as for the sparse evaluation, there is no double backward.
  *
  * The handle is host data only, as for cgtp_norm. */
 typedef struct cgtp_router_s* cgtp_router;
@@ -452,9 +460,12 @@ cgtp_status cgtp_router_destroy(cgtp_router router); /* NULL is accepted */
  *     multiple of 4, so that every row is 16-byte aligned; columns from n on
  *     are left as they were
  *   counts [n_experts] int32: rows given to each expert
- * Each output may be NULL (not written); the others are overwritten.  Bitwise
- * reproducible (the only atomics add integers).  Nothing is allocated; the call
- * can be captured.  Errors: NULL, SIZE, ALIGN, CUDA. */
+ * Each output may be NULL (not written); the others are overwritten.  The same
+ * call gives the same bits (the only atomics add integers); with another number
+ * of rows a row's ids stay the same, its weights up to their rounding (a weight
+ * is within 160 2^-24 of itself, one of a score below the smallest normal float
+ * within that times scale).  Nothing is allocated; the call can be captured.
+ * Errors: NULL, SIZE, ALIGN, CUDA. */
 cgtp_status cgtp_router_forward(cgtp_router router, int64_t n, const float* logits, const float* bias,
                                 int32_t* ids, float* weights, float* gates, int64_t ld, int32_t* counts,
                                 cgtp_stream stream);

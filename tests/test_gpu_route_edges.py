@@ -164,3 +164,15 @@ def test_dominant_score_listed_twice(dev):
     p /= p.sum(1, keepdims=True)
     mag += 2 / 320 * np.abs(d).sum(1, keepdims=True) * p * np.where(np.arange(16) == top[:, None], 1 - p, 1)
     assert (np.abs(got - ref) <= 320 * U * mag + 1e-37).all(), float((np.abs(got - ref) / (U * mag + 1e-37)).max())
+
+
+def test_large_logits_of_sigmoids(dev):
+    """Saturated sigmoids are chosen by their logits, infinite ones as the
+    largest float; those below the smallest float keep their order."""
+    big = float(np.finfo(np.float32).max)
+    l = np.array([[np.inf, 1.0, 2.0, np.inf], [big, big, 0.0, 1.0], [300.0, 200.0, -300.0, 0.0],
+                  [-300.0, -301.0, -299.5, -400.0], [-3e38, -3.1e38, -np.inf, -3.2e38]], np.float32)
+    for k in (1, 2, 3):
+        for n in (5, 20000):
+            choices(l, None, dict(k=k, score="sigmoid", renormalise=False), dev, n)
+            choices(l[:4], None, dict(k=k, score="sigmoid"), dev, n)
