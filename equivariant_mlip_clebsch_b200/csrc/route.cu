@@ -1013,7 +1013,7 @@ __global__ void __launch_bounds__(2 * kRows, K <= 8 ? 5 : 2) route_chosen_backwa
         }
         l[j] = fminf(l[j], FLT_MAX);
       }
-      float m = 0.f, sum = 0.f, dot = 0.f, ref = 0.f;
+      float m = 0.f, sum = 0.f, dot = 0.f;
       if (p.renormalise) {
         m = -FLT_MAX;
 #pragma unroll
@@ -1043,9 +1043,14 @@ __global__ void __launch_bounds__(2 * kRows, K <= 8 ? 5 : 2) route_chosen_backwa
         for (int j = 0; j < K; ++j)
           if (id[j] >= 0) {
             share[j] /= sum;
-            if (K > 8 && share[j] > 0.5f) ref = d[j];
+            dot = fmaf(d[j], share[j], dot);
           }
-        if (K > 8) {
+        if constexpr (K > 8) {
+          float ref = 0.f;
+          dot = 0.f;
+#pragma unroll
+          for (int j = 0; j < K; ++j)
+            if (id[j] >= 0 && share[j] > 0.5f) ref = d[j];
 #pragma unroll
           for (int j = 0; j < K; ++j)
             if (id[j] >= 0) {
