@@ -346,10 +346,10 @@ __device__ __forceinline__ void norm_rows(const NormSeg& s, int o, int D, float 
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int e = 4 * q + j;
-            const float xh = x[e] * r;
             gq[j] = g[e];
-            p[j] = g[e] * xh;
-            y[j] = fmaf(xh, along, CENTRED ? fmaf(g[e] * w[j], r, shift) : g[e] * w[j] * r);
+            x[e] *= r;
+            p[j] = g[e] * x[e];
+            y[j] = fmaf(x[e], along, CENTRED ? fmaf(g[e], w[j] * r, shift) : g[e] * (w[j] * r));
           }
           if (a.out) store4<SHIFT>(a.out + at + 4 * q * W, whole, some, y);
           if (dw) add_to(acc[q * T], make_float4(p[0], p[1], p[2], p[3]));
