@@ -201,9 +201,12 @@ __device__ __forceinline__ void add_to(float4& acc, const float4 v) {
 // What bounds it (B200, 6,144 rows of 256x0e+352x1o+384x2e+320x3o): the backward
 // moves its 403 MB at 5.5 TB/s, 84 % of the measured copy rate, with 32 warps an
 // SM; the forward of 768 rows of 52,864 columns 325 MB at 5.3 TB/s, 82 %; the
-// double backward of 6,144 x 704 (in L2) 86 MB in 20 us, held by the latency that
-// 16 warps an SM of 122 registers leave open (24 warps of 80 registers: 21 us, 32 of
-// 64: 24 us, for their spills).  Few rows cost their launches: 2 us and 7 us.
+// double backward of 6,144 x 704 (in L2) 86 MB in 17.5 us, held by the latency that
+// 16 warps an SM of 119 registers leave open (24 warps of 80 registers took 5 % more,
+// 32 of 64 20 %, for their spills).  Few rows cost their launches: 2.5 us and 7 us.
+// Rows that start anywhere, 6,143 x 5,456: forward 54 us, backward 84, double 203 (on
+// 16-byte borders 52, 74, 134); with 32 values a thread the double backward spills (504
+// bytes stored, 1,060 loaded): 768 rows of Lmax 6 312 us, on 16-byte borders 188.
 template <int OP, int T, int V, bool SHIFT, bool CENTRED, int TLOG>
 __device__ __forceinline__ void norm_rows(const NormSeg& s, int o, int D, float eps, int64_t n, const NormArgs& a,
                                           bool dw, bool db, const float4* sw, const float4* s2, const float4* s3,
@@ -519,7 +522,9 @@ __global__ void __launch_bounds__(kFinish) norm_finish_kernel(const __grid_const
   if (lane == 0 && mine < mul) out[mine] = v;
 }
 
-// ---- blocks wider than the registers of a CTA: one CTA a unit, several reads
+// ---- blocks wider than the registers of a CTA: one CTA a unit, several reads, and one
+// CTA a channel for the weights, which reads columns.  768 rows of 40000x0e (123 MB an
+// array), us: forward 154, backward 569, double backward 893: 4, 10 and 9.5 times what the bytes take
 
 constexpr int kWide = 256;
 
